@@ -1,4 +1,5 @@
-"""ctypes view of libsage.so (the C ABI declared in include/sage.h and include/sage_nvfp4.h).
+"""ctypes view of libsage.so (the C ABI declared in include/sage.h, include/sage_nvfp4.h and
+include/sage_packed.h).
 
 Loading fails loudly when the shared library is missing: there is no fallback path.
 """
@@ -40,6 +41,32 @@ class SageFp4Bufs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("q_fp4", "k_fp4", "q_sf", "k_sf", "q_genc", "k_genc", "q_inv_rms",
                  "k_inv_rms", "k_mean", "q_fp4_t", "k_fp4_t", "q_sf_t", "k_sf_t")]
+
+
+class SageRows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class SageRopeParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("sections", ctypes.c_int * 4), ("inv_freq", ctypes.c_void_p),
+                ("pos_bits", ctypes.c_int), ("pos_axis_stride", ctypes.c_int64),
+                ("pos_batch_stride", ctypes.c_int64)]
+
+
+class SagePackedInfo(ctypes.Structure):
+    _fields_ = [("sequences", ctypes.c_int), ("tiles", ctypes.c_int), ("pairs", ctypes.c_int),
+                ("longest", ctypes.c_int), ("tokens", ctypes.c_int64)]
+
+
+class SagePackedParams(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("causal", ctypes.c_int),
+                ("softmax_scale", ctypes.c_float)]
 
 
 class SageError(RuntimeError):
@@ -116,6 +143,23 @@ def lib() -> ctypes.CDLL:
         L.sage_debug_wait_timeout.restype = i
         L.sage_mma_peak.argtypes = [i, i, i, vp, sz, vp]
         L.sage_mma_peak.restype = i
+        R, RP, PI, PP = P(SageRows), P(SageRopeParams), P(SagePackedInfo), P(SagePackedParams)
+        L.sage_qk_norm_rope_fwd.argtypes = [RP, R, R, vp, vp, vp, R, R, vp]
+        L.sage_qk_norm_rope_fwd.restype = i
+        L.sage_qk_norm_rope_workspace_bytes.argtypes = [RP]
+        L.sage_qk_norm_rope_workspace_bytes.restype = sz
+        L.sage_qk_norm_rope_bwd.argtypes = [RP, R, R, vp, vp, vp, R, R, R, R, vp, vp, vp, sz, vp]
+        L.sage_qk_norm_rope_bwd.restype = i
+        L.sage_packed_plan_bytes.argtypes = [P(ctypes.c_int), i]
+        L.sage_packed_plan_bytes.restype = sz
+        L.sage_packed_plan_fill.argtypes = [P(ctypes.c_int), i, vp, sz, PI]
+        L.sage_packed_plan_fill.restype = i
+        L.sage_packed_attn_fwd.argtypes = [PP, PI, vp, R, R, R, R, vp, vp]
+        L.sage_packed_attn_fwd.restype = i
+        L.sage_packed_attn_bwd_workspace_bytes.argtypes = [PP, PI]
+        L.sage_packed_attn_bwd_workspace_bytes.restype = sz
+        L.sage_packed_attn_bwd.argtypes = [PP, PI, vp, R, R, R, R, vp, R, R, R, R, vp, sz, vp]
+        L.sage_packed_attn_bwd.restype = i
         _lib = L
     return _lib
 

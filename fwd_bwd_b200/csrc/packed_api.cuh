@@ -1,0 +1,499 @@
+// packed_api.cuh -- host side of include/sage_packed.h: argument checks, the packed plan, tensor
+// maps and launches.  Included once, by sage_api.cu (one translation unit).
+#pragma once
+
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "packed_bwd.cuh"
+#include "packed_fwd.cuh"
+#include "qk_rope.cuh"
+#include "sage_packed.h"
+
+namespace {
+
+using sage::packed::Item;
+
+int check_rows(const sage_rows* r, int64_t batches, int64_t tokens, int heads, int d, bool out) {
+  if (!r || !r->ptr) return SAGE_ERR_INVALID_ARG;
+  if (!aligned16(r->ptr)) return SAGE_ERR_ALIGNMENT;
+  const int64_t n[3] = {batches, tokens, heads};
+  const int64_t s[3] = {r->batch_stride, r->token_stride, r->head_stride};
+  constexpr int64_t kMost = int64_t{1} << 38;  // elements; byte strides stay below 2^40
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) continue;  // the stride of a single entry is never used
+    if (s[i] < d || s[i] > kMost) return SAGE_ERR_INVALID_ARG;
+    if (s[i] % 8 != 0) return SAGE_ERR_ALIGNMENT;
+  }
+  if (out) {  // no two vectors of an output may overlap: sorted by stride, each axis must clear
+              // the extent of the ones inside it
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int x, int y) { return s[x] < s[y]; });
+    int64_t extent = d;
+    for (int i : order) {
+      if (n[i] == 1) continue;
+      if (s[i] < extent) return SAGE_ERR_INVALID_ARG;
+      extent += s[i] * (n[i] - 1);
+    }
+  }
+  return SAGE_OK;
+}
+
+// ---- QK-norm and rotary positions ---------------------------------------------------------
+int check_rope(const sage_rope_params* p) {
+  if (!p || p->B <= 0 || p->N <= 0 || p->Hq <= 0 || p->Hkv <= 0) return SAGE_ERR_INVALID_ARG;
+  if (p->dtype != SAGE_FP16 && p->dtype != SAGE_BF16) return SAGE_ERR_INVALID_ARG;
+  if (p->d != 64 && p->d != 128) return SAGE_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p->B) * p->N >= (int64_t{1} << 31) || p->Hq > 65536 ||
+      p->Hkv > 65536)
+    return SAGE_ERR_UNSUPPORTED;
+  if ((p->norm != 0 && p->norm != 1) || (p->interleaved != 0 && p->interleaved != 1))
+    return SAGE_ERR_INVALID_ARG;
+  if (!(p->eps >= 0.0f) || !std::isfinite(p->eps)) return SAGE_ERR_INVALID_ARG;
+  if (p->rotary_dim < 0 || p->rotary_dim > p->d) return SAGE_ERR_INVALID_ARG;
+  if (p->rotary_dim % 16 != 0) return SAGE_ERR_UNSUPPORTED;
+  if (p->rotary_dim > 0) {
+    if (!p->inv_freq || (p->pos_bits != 32 && p->pos_bits != 64)) return SAGE_ERR_INVALID_ARG;
+    if (p->n_axes < 1 || p->n_axes > sage::rope::kMaxAxes) return SAGE_ERR_INVALID_ARG;
+    int64_t sum = 0;
+    for (int i = 0; i < p->n_axes; ++i) {
+      if (p->sections[i] <= 0) return SAGE_ERR_INVALID_ARG;
+      sum += p->sections[i];
+    }
+    if (sum != p->rotary_dim / 2) return SAGE_ERR_INVALID_ARG;
+    for (int i = 0; i < p->rotary_dim / 2; ++i)
+      if (!std::isfinite(p->inv_freq[i])) return SAGE_ERR_INVALID_ARG;
+    if (p->pos_axis_stride < 0 || p->pos_batch_stride < 0) return SAGE_ERR_INVALID_ARG;
+  }
+  return SAGE_OK;
+}
+
+// inv_freq / (2 pi) as a fraction of a turn per position, in units of 2^-64 turns.
+uint64_t turn_fraction(double inv_freq) {
+  const long double turns = static_cast<long double>(inv_freq) /
+                            6.283185307179586476925286766559005768L;
+  const long double frac = turns - std::floor(turns);  // [0, 1]
+  const long double scaled = frac * 18446744073709551616.0L;
+  return scaled >= 18446744073709551615.0L ? 0 : static_cast<uint64_t>(scaled + 0.5L);
+}
+
+sage::rope::Rows rope_rows(const sage_rows* r) {
+  return {static_cast<char*>(r->ptr), r->batch_stride, r->token_stride, r->head_stride};
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+// Blocks of the gradient kernel at most: their partial sums of the gains' gradients are added
+// up by one small kernel, so their number is kept to four per SM of a 148-SM device.
+constexpr int kRopeBwdBlocks = 592;
+
+void rope_args(const sage_rope_params* p, sage::rope::Args* a) {
+  std::memset(a, 0, sizeof(*a));
+  a->tokens = p->B * p->N;
+  a->N = p->N;
+  a->Hq = p->Hq;
+  a->Hkv = p->Hkv;
+  a->rotary = p->rotary_dim;
+  a->interleaved = p->interleaved;
+  a->norm = p->norm;
+  a->eps = p->eps;
+  for (int& b : a->bound) b = 64;  // beyond the last pair
+  if (p->rotary_dim > 0) {
+    a->n_axes = p->n_axes;
+    a->pos64 = p->pos_bits == 64;
+    a->pos_as = p->pos_axis_stride;
+    a->pos_bs = p->pos_batch_stride;
+    for (int i = 0; i < p->rotary_dim / 2; ++i) a->freq[i] = turn_fraction(p->inv_freq[i]);
+    for (int i = 0, at = 0; i + 1 < p->n_axes; ++i) a->bound[i] = at += p->sections[i];
+  }
+  // Heads of a token per lane group: all of them when there are tokens enough to fill the
+  // device (the angles are then computed once per token), fewer otherwise.
+  const int H = p->Hq + p->Hkv;
+  const int want = 2 * 148 * 1024 / (p->d / 8);  // lane groups that keep the memory system busy
+  const int chunks = std::max(1, std::min(H, (want + a->tokens - 1) / a->tokens));
+  a->per_chunk = (H + chunks - 1) / chunks;
+  a->chunks = (H + a->per_chunk - 1) / a->per_chunk;
+}
+
+template <typename T, int D, bool BWD>
+int run_rope(sage::rope::Args* a, float* dgain_q, float* dgain_k, cudaStream_t st) {
+  const int groups = sage::rope::kThreads / (D / 8);
+  const int64_t units = static_cast<int64_t>(a->tokens) * a->chunks;
+  const int64_t need = (units + groups - 1) / groups;
+  const int sms = sm_count();
+  if (sms == 0) return SAGE_ERR_CUDA;
+  const int64_t most = BWD ? std::min(kRopeBwdBlocks, 4 * sms) : 8 * sms;
+  const int blocks = static_cast<int>(std::min(need, most));
+  sage::rope::qk_rope_kernel<T, D, BWD><<<blocks, sage::rope::kThreads, 0, st>>>(*a);
+  if (BWD && a->partial)
+    sage::rope::dgain_kernel<D><<<2 * D / 32, 1024, 0, st>>>(a->partial, blocks, dgain_q, dgain_k);
+  return launch_status();
+}
+
+template <bool BWD>
+int launch_rope(const sage_rope_params* p, sage::rope::Args* a, float* dgain_q, float* dgain_k,
+                cudaStream_t st) {
+  const bool bf = p->dtype == SAGE_BF16;
+  if (p->d == 128)
+    return bf ? run_rope<__nv_bfloat16, 128, BWD>(a, dgain_q, dgain_k, st)
+              : run_rope<__half, 128, BWD>(a, dgain_q, dgain_k, st);
+  return bf ? run_rope<__nv_bfloat16, 64, BWD>(a, dgain_q, dgain_k, st)
+            : run_rope<__half, 64, BWD>(a, dgain_q, dgain_k, st);
+}
+
+// ---- packed plan --------------------------------------------------------------------------
+// Four lists of Items, each largest work first: query / key tiles under a causal mask (the
+// work of query tile t is t + 1 key tiles; key tile tiles - 1 - t has the same), the same without
+// (every tile of a sequence works over all of its tiles), then pairs of neighbouring tiles
+// (named by the later one, cut from the sequence's end) in the same two orders.
+bool plan_counts(const int* lengths, int n, sage_packed_info* info) {
+  if (!lengths || n < 1) return false;
+  int64_t tokens = 0, tiles = 0, pairs = 0;
+  int longest = 0;
+  for (int i = 0; i < n; ++i) {
+    if (lengths[i] < 0) return false;
+    tokens += lengths[i];
+    if (tokens >= (int64_t{1} << 31) - sage::packed::BT) return false;
+    const int64_t t = (static_cast<int64_t>(lengths[i]) + sage::packed::BT - 1) / sage::packed::BT;
+    tiles += t;
+    pairs += (t + 1) / 2;
+    longest = std::max(longest, lengths[i]);
+  }
+  info->sequences = n;
+  info->tiles = static_cast<int>(tiles);
+  info->pairs = static_cast<int>(pairs);
+  info->longest = longest;
+  info->tokens = tokens;
+  return true;
+}
+
+size_t plan_bytes(const sage_packed_info& i) {
+  return sizeof(Item) * 2 * (static_cast<size_t>(i.tiles) + i.pairs) + sizeof(Item);
+}
+const Item* plan_list(const void* plan, const sage_packed_info* i, bool causal, bool pairs) {
+  const Item* p = static_cast<const Item*>(plan);
+  if (pairs) return p + 2 * static_cast<size_t>(i->tiles) + (causal ? 0 : i->pairs);
+  return p + (causal ? 0 : i->tiles);
+}
+
+int check_packed(const sage_packed_params* p, const sage_packed_info* info, const void* plan) {
+  if (!p || !info || !plan) return SAGE_ERR_INVALID_ARG;
+  if (p->T <= 0 || p->Hq <= 0 || p->Hkv <= 0 || p->Hq % p->Hkv != 0) return SAGE_ERR_INVALID_ARG;
+  if (p->dtype != SAGE_FP16 && p->dtype != SAGE_BF16) return SAGE_ERR_INVALID_ARG;
+  if (p->causal != 0 && p->causal != 1) return SAGE_ERR_INVALID_ARG;
+  if (!std::isfinite(p->softmax_scale)) return SAGE_ERR_INVALID_ARG;
+  if (p->d != 64 && p->d != 128) return SAGE_ERR_UNSUPPORTED;
+  if (p->T >= (int64_t{1} << 31) || p->Hq > 65536) return SAGE_ERR_UNSUPPORTED;
+  if (info->sequences < 1 || info->tiles < 0 || info->pairs < 0 || info->pairs > info->tiles ||
+      info->tokens < 0 || info->tokens > p->T)
+    return SAGE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(info->tiles) * p->Hq >= (int64_t{1} << 31)) return SAGE_ERR_UNSUPPORTED;
+  if (!aligned16(plan)) return SAGE_ERR_ALIGNMENT;
+  return SAGE_OK;
+}
+
+float packed_tau(const sage_packed_params* p) {
+  return p->softmax_scale > 0.0f ? p->softmax_scale
+                                 : 1.0f / std::sqrt(static_cast<float>(p->d));
+}
+
+// 4-D map (channel, row of a tile, token, head) of 16-bit rows: the row and the token axis have
+// the same stride, so a box that starts at a negative row reads zeros there.  The box is 64
+// channels x 128 rows (rows of 128 bytes, swizzled).
+bool make_tile_map(CUtensorMap* m, const sage_rows* r, const sage_packed_params* p, int heads) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t ts = p->T > 1 ? r->token_stride : p->d;
+  const cuuint64_t hs = heads > 1 ? r->head_stride : p->d;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(p->d), sage::packed::BT,
+                        static_cast<cuuint64_t>(p->T), static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[3] = {ts * 2, ts * 2, hs * 2};
+  cuuint32_t box[4] = {64, sage::packed::BT, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, r->ptr, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+sage::packed::Out packed_out(const sage_rows* r) {
+  return {static_cast<char*>(r->ptr), r->token_stride, r->head_stride};
+}
+
+template <typename K, typename... A>
+int launch_packed(K kern, int regs, int64_t grid, int threads, size_t smem, cudaStream_t st,
+                  const A&... args) {
+  if (set_smem(kern, smem) != SAGE_OK) return SAGE_ERR_CUDA;
+  // the kernels move registers between warpgroups (setmaxnreg); the split is sized for exactly
+  // this launch allocation
+  if (launch_regs(kern) != regs) return SAGE_ERR_UNSUPPORTED;
+  kern<<<static_cast<unsigned>(grid), threads, smem, st>>>(args...);
+  return launch_status();
+}
+
+template <typename T, int D>
+int run_packed_fwd(const sage_packed_params* p, const sage_packed_info* info, const void* plan,
+                   const sage_rows* q, const sage_rows* k, const sage_rows* v, const sage_rows* o,
+                   float* lse, cudaStream_t st) {
+  namespace F = sage::packed::fwd;
+  CUtensorMap tq, tk, tv;
+  if (!make_tile_map(&tq, q, p, p->Hq) || !make_tile_map(&tk, k, p, p->Hkv) ||
+      !make_tile_map(&tv, v, p, p->Hkv))
+    return SAGE_ERR_CUDA;
+  F::Args a;
+  a.group = p->Hq / p->Hkv;
+  const bool heads = a.group % 2 == 0;
+  a.items = plan_list(plan, info, p->causal, !heads);
+  a.o = packed_out(o);
+  a.lse = lse;
+  a.T = p->T;
+  a.head_groups = heads ? p->Hq / 2 : p->Hq;
+  a.causal = p->causal;
+  a.scale_log2 = packed_tau(p) * 1.4426950408889634f;
+  const int64_t grid = static_cast<int64_t>(heads ? info->tiles : info->pairs) * a.head_groups;
+  return heads ? launch_packed(F::attn_fwd_kernel<T, D, true>, F::kLaunchRegs, grid, F::kThreads,
+                               F::smem_bytes<T, D>(), st, tq, tk, tv, a)
+               : launch_packed(F::attn_fwd_kernel<T, D, false>, F::kLaunchRegs, grid, F::kThreads,
+                               F::smem_bytes<T, D>(), st, tq, tk, tv, a);
+}
+
+// Workspace: D [Hq][T]; in half precision also the norms [sequences][Hkv][2].
+struct PackedWs {
+  size_t norms, norms_bytes, total;
+};
+PackedWs packed_ws(const sage_packed_params* p, const sage_packed_info* info) {
+  PackedWs w;
+  w.norms = align_up(static_cast<size_t>(p->Hq) * p->T * 4);
+  w.norms_bytes =
+      p->dtype == SAGE_FP16 ? static_cast<size_t>(info->sequences) * p->Hkv * 2 * 4 : 0;
+  w.total = align_up(w.norms + w.norms_bytes);
+  return w;
+}
+
+template <typename T, int D>
+int run_packed_bwd(const sage_packed_params* p, const sage_packed_info* info, const void* plan,
+                   const sage_rows* q, const sage_rows* k, const sage_rows* v, const sage_rows* o,
+                   const float* lse, const sage_rows* dout, const sage_rows* dq,
+                   const sage_rows* dk, const sage_rows* dv, void* ws, cudaStream_t st) {
+  namespace B = sage::packed::bwd;
+  constexpr bool kNorms = B::Scaling<T>::kOn;
+  CUtensorMap tq, tk, tv, tdo;
+  if (!make_tile_map(&tq, q, p, p->Hq) || !make_tile_map(&tk, k, p, p->Hkv) ||
+      !make_tile_map(&tv, v, p, p->Hkv) || !make_tile_map(&tdo, dout, p, p->Hq))
+    return SAGE_ERR_CUDA;
+  const PackedWs w = packed_ws(p, info);
+  B::RowArgs r;
+  r.o = packed_out(o);
+  r.dout = packed_out(dout);
+  r.v = packed_out(v);
+  r.items = plan_list(plan, info, p->causal, false);
+  r.dvec = static_cast<float*>(ws);
+  r.norms = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + w.norms);
+  r.T = p->T;
+  r.tiles = info->tiles;
+  r.Hq = p->Hq;
+  r.Hkv = p->Hkv;
+  r.group = p->Hq / p->Hkv;
+  if (kNorms && cudaMemsetAsync(r.norms, 0, w.norms_bytes, st) != cudaSuccess)
+    return SAGE_ERR_CUDA;
+  const int64_t row_ctas =
+      static_cast<int64_t>(info->tiles) * (p->Hq + (kNorms ? p->Hkv : 0));
+  B::row_kernel<T, D, kNorms>
+      <<<static_cast<unsigned>(row_ctas), B::kRowKernelThreads, 0, st>>>(r);
+  int s = launch_status();
+  if (s != SAGE_OK) return s;
+  B::Args a;
+  a.items = r.items;
+  a.lse = lse;
+  a.dvec = r.dvec;
+  a.norms = r.norms;
+  a.T = p->T;
+  a.group = r.group;
+  a.causal = p->causal;
+  a.tau = packed_tau(p);
+  a.scale_log2 = a.tau * 1.4426950408889634f;
+  a.heads = p->Hkv;
+  a.out[0] = packed_out(dv);
+  a.out[1] = packed_out(dk);
+  s = launch_packed(B::dkv_kernel<T, D>, B::kLaunchRegs,
+                    static_cast<int64_t>(info->tiles) * p->Hkv, B::kThreads,
+                    B::dkv_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
+  if (s != SAGE_OK) return s;
+  a.heads = p->Hq;
+  a.out[0] = packed_out(dq);
+  return launch_packed(B::dq_kernel<T, D>, B::kLaunchRegs,
+                       static_cast<int64_t>(info->tiles) * p->Hq, B::kThreads,
+                       B::dq_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+int sage_qk_norm_rope_fwd(const sage_rope_params* p, const sage_rows* q, const sage_rows* k,
+                          const float* gain_q, const float* gain_k, const void* pos,
+                          const sage_rows* q_out, const sage_rows* k_out, void* stream) {
+  int s = check_rope(p);
+  if (s != SAGE_OK) return s;
+  const sage_rows* rows[4] = {q, k, q_out, k_out};
+  for (int i = 0; i < 4; ++i)
+    if ((s = check_rows(rows[i], p->B, p->N, i % 2 ? p->Hkv : p->Hq, p->d, i >= 2)) != SAGE_OK)
+      return s;
+  if (p->rotary_dim > 0 && !pos) return SAGE_ERR_INVALID_ARG;
+  if (!p->norm && (gain_q || gain_k)) return SAGE_ERR_INVALID_ARG;
+  sage::rope::Args a;
+  rope_args(p, &a);
+  for (int w = 0; w < 2; ++w) {
+    a.x[w] = rope_rows(w ? k : q);
+    a.y[w] = rope_rows(w ? k_out : q_out);
+    a.gain[w] = w ? gain_k : gain_q;
+  }
+  a.pos = pos;
+  return launch_rope<false>(p, &a, nullptr, nullptr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t sage_qk_norm_rope_workspace_bytes(const sage_rope_params* p) {
+  if (check_rope(p) != SAGE_OK) return 0;
+  return align_up(static_cast<size_t>(kRopeBwdBlocks) * 2 * p->d * 4);
+}
+
+int sage_qk_norm_rope_bwd(const sage_rope_params* p, const sage_rows* q, const sage_rows* k,
+                          const float* gain_q, const float* gain_k, const void* pos,
+                          const sage_rows* dq_out, const sage_rows* dk_out, const sage_rows* dq,
+                          const sage_rows* dk, float* dgain_q, float* dgain_k, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  int s = check_rope(p);
+  if (s != SAGE_OK) return s;
+  const sage_rows* rows[6] = {q, k, dq_out, dk_out, dq, dk};
+  for (int i = 0; i < 6; ++i)
+    if ((s = check_rows(rows[i], p->B, p->N, i % 2 ? p->Hkv : p->Hq, p->d, i >= 4)) != SAGE_OK)
+      return s;
+  if (p->rotary_dim > 0 && !pos) return SAGE_ERR_INVALID_ARG;
+  if (!p->norm && (gain_q || gain_k || dgain_q || dgain_k)) return SAGE_ERR_INVALID_ARG;
+  if ((dgain_q == nullptr) != (dgain_k == nullptr)) return SAGE_ERR_INVALID_ARG;
+  if (dgain_q) {
+    if (!workspace || workspace_bytes < sage_qk_norm_rope_workspace_bytes(p))
+      return SAGE_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SAGE_ERR_ALIGNMENT;
+  }
+  sage::rope::Args a;
+  rope_args(p, &a);
+  for (int w = 0; w < 2; ++w) {
+    a.x[w] = rope_rows(w ? k : q);
+    a.g[w] = rope_rows(w ? dk_out : dq_out);
+    a.y[w] = rope_rows(w ? dk : dq);
+    a.gain[w] = w ? gain_k : gain_q;
+  }
+  a.pos = pos;
+  a.partial = dgain_q ? static_cast<float*>(workspace) : nullptr;
+  return launch_rope<true>(p, &a, dgain_q, dgain_k, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t sage_packed_plan_bytes(const int* lengths, int sequences) {
+  sage_packed_info info;
+  return plan_counts(lengths, sequences, &info) ? plan_bytes(info) : 0;
+}
+
+int sage_packed_plan_fill(const int* lengths, int sequences, void* host_plan, size_t bytes,
+                          sage_packed_info* info) {
+  sage_packed_info in;
+  if (!host_plan || !info || !plan_counts(lengths, sequences, &in)) return SAGE_ERR_INVALID_ARG;
+  if (bytes < plan_bytes(in)) return SAGE_ERR_WORKSPACE;
+  try {
+    // counting sort by descending work, sequences in order within one amount of work
+    const int most = (in.longest + sage::packed::BT - 1) / sage::packed::BT;
+    Item* out = static_cast<Item*>(host_plan);
+    std::memset(out, 0, plan_bytes(in));
+    for (int list = 0; list < 4; ++list) {
+      const bool pairs = list >= 2, causal = list % 2 == 0;
+      const int count = pairs ? in.pairs : in.tiles;
+      std::vector<int> at(static_cast<size_t>(most) + 2, 0);  // at[most - work]: next place
+      for (int pass = 0; pass < 2; ++pass) {
+        for (int i = 0, start = 0; i < sequences; start += lengths[i], ++i) {
+          const int tiles = static_cast<int>(
+              (static_cast<int64_t>(lengths[i]) + sage::packed::BT - 1) / sage::packed::BT);
+          for (int t = tiles - 1; t >= 0; t -= pairs ? 2 : 1) {
+            const int slot = most - (causal ? t + 1 : tiles);
+            if (pass == 0)
+              ++at[slot + 1];
+            else
+              out[at[slot]++] = Item{start, lengths[i], t, i};
+          }
+        }
+        if (pass == 0)
+          for (int w = 0; w <= most; ++w) at[w + 1] += at[w];
+      }
+      out += count;
+    }
+  } catch (const std::bad_alloc&) {
+    return SAGE_ERR_WORKSPACE;
+  }
+  *info = in;
+  return SAGE_OK;
+}
+
+int sage_packed_attn_fwd(const sage_packed_params* p, const sage_packed_info* info,
+                         const void* plan, const sage_rows* q, const sage_rows* k,
+                         const sage_rows* v, const sage_rows* o, float* lse, void* stream) {
+  int s = check_packed(p, info, plan);
+  if (s != SAGE_OK) return s;
+  const sage_rows* rows[4] = {q, k, v, o};
+  for (int i = 0; i < 4; ++i)
+    if ((s = check_rows(rows[i], 1, p->T, i == 1 || i == 2 ? p->Hkv : p->Hq, p->d, i == 3)) !=
+        SAGE_OK)
+      return s;
+  if (!lse) return SAGE_ERR_INVALID_ARG;
+  if (info->tiles == 0) return SAGE_OK;  // only empty sequences: nothing to write
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = p->dtype == SAGE_BF16;
+  if (p->d == 128)
+    return bf ? run_packed_fwd<__nv_bfloat16, 128>(p, info, plan, q, k, v, o, lse, st)
+              : run_packed_fwd<__half, 128>(p, info, plan, q, k, v, o, lse, st);
+  return bf ? run_packed_fwd<__nv_bfloat16, 64>(p, info, plan, q, k, v, o, lse, st)
+            : run_packed_fwd<__half, 64>(p, info, plan, q, k, v, o, lse, st);
+}
+
+size_t sage_packed_attn_bwd_workspace_bytes(const sage_packed_params* p,
+                                            const sage_packed_info* info) {
+  alignas(16) static const char some[16] = {};
+  if (check_packed(p, info, some) != SAGE_OK) return 0;
+  return packed_ws(p, info).total;
+}
+
+int sage_packed_attn_bwd(const sage_packed_params* p, const sage_packed_info* info,
+                         const void* plan, const sage_rows* q, const sage_rows* k,
+                         const sage_rows* v, const sage_rows* o, const float* lse,
+                         const sage_rows* dout, const sage_rows* dq, const sage_rows* dk,
+                         const sage_rows* dv, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  int s = check_packed(p, info, plan);
+  if (s != SAGE_OK) return s;
+  const sage_rows* rows[8] = {q, o, dout, dq, k, v, dk, dv};
+  for (int i = 0; i < 8; ++i)
+    if ((s = check_rows(rows[i], 1, p->T, i >= 4 ? p->Hkv : p->Hq, p->d,
+                        i == 3 || i >= 6)) != SAGE_OK)
+      return s;
+  if (!lse) return SAGE_ERR_INVALID_ARG;
+  if (info->tiles == 0) return SAGE_OK;
+  if (!workspace || workspace_bytes < packed_ws(p, info).total) return SAGE_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return SAGE_ERR_ALIGNMENT;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = p->dtype == SAGE_BF16;
+  if (p->d == 128)
+    return bf ? run_packed_bwd<__nv_bfloat16, 128>(p, info, plan, q, k, v, o, lse, dout, dq, dk,
+                                                   dv, workspace, st)
+              : run_packed_bwd<__half, 128>(p, info, plan, q, k, v, o, lse, dout, dq, dk, dv,
+                                            workspace, st);
+  return bf ? run_packed_bwd<__nv_bfloat16, 64>(p, info, plan, q, k, v, o, lse, dout, dq, dk, dv,
+                                                workspace, st)
+            : run_packed_bwd<__half, 64>(p, info, plan, q, k, v, o, lse, dout, dq, dk, dv,
+                                         workspace, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,647 @@
+// packed_bwd.cuh -- backward of the 16-bit attention over packed sequences with grouped heads.
+//
+//   P_ij = exp(tau q_i . k_j - LSE_i), D_i = dO_i . O_i, dS_ij = P_ij (dO_i . v_j - D_i)
+//   dV_j = sum_{h,i} P_ij dO_i,  dK_j = tau sum_{h,i} dS_ij q_i,  dQ_i = tau sum_j dS_ij k_j
+// (h over the query heads that share j's key head).  Tiles and tensor maps as in the forward.
+//
+// Two kernels after the row pass that forms D, each recomputing S and dP for its own direction:
+//   * dkv_kernel: one CTA per (key tile, key head), walking the query tiles of every head of the
+//     group.  It works on transposed tiles (rows = keys), so P^T and dS^T go from registers to
+//     TMEM as the A operands of dV += P^T dO and dK += dS^T Q, and dV, dK stay in TMEM;
+//   * dq_kernel: one CTA per (query tile, query head), walking the key tiles: dQ += dS K.
+// Seven products where one fused pass would need five, but no gradient is ever added up across
+// CTAs: no atomics, no float32 accumulator in HBM, no finishing pass, the same bits every run,
+// and grouped heads cost nothing extra.
+//
+// Both: warps 0-7 compute (a thread holds half a row, 64 columns: warps 0-3 the first half),
+// warp 8 TMA producer, warp 9 MMA issuer, warps 10-11 complete the warpgroup; in dkv_kernel warp
+// 10 brings the query rows' LSE and D to shared memory.
+//
+// Rounding: P and dS to the tensors' type for their products; sums in float32; outputs once.
+// Half precision: P is multiplied by 2^14 before it is rounded, and dS by the power of two that
+// puts the bound 2 max |dO_i| max |v_j| of |dP - D| (over the sequence and key head) at 2^15 or
+// just below: small values keep their bits, nothing overflows, and the factors are taken out of
+// the float32 sums exactly.
+#pragma once
+
+#include "packed_fwd.cuh"
+
+namespace sage {
+namespace packed {
+namespace bwd {
+
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kRowWarp = 10;
+constexpr int kLaunchRegs = 168, kComputeRegs = 232, kOtherRegs = 40;
+static_assert(256 * kComputeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T>
+struct Scaling {
+  static constexpr bool kOn = false;
+  static constexpr float kPShift = 0.0f;  // log2 of P's factor
+};
+template <>
+struct Scaling<__half> {
+  static constexpr bool kOn = true;
+  static constexpr float kPShift = 14.0f;
+};
+
+// ---- row pass: D_i = dO_i . O_i; half precision also the largest |dO_i|^2 and |v_j|^2 ---------
+struct RowArgs {
+  Out o, dout, v;        // inputs
+  const Item* items;
+  float* dvec;           // [Hq][T]
+  uint32_t* norms;       // [sequences][Hkv][2]: bits of max |dO|^2, max |v|^2 (zeroed before)
+  int64_t T;
+  int tiles, Hq, Hkv, group;
+};
+
+constexpr int kRowKernelThreads = 256;
+
+// One CTA per (tile, query head); with NORMS, then per (tile, key head) for v.
+template <typename T, int D, bool NORMS>
+__global__ void __launch_bounds__(kRowKernelThreads) row_kernel(const RowArgs a) {
+  constexpr int LPR = D / 8, ROWS = kRowKernelThreads / LPR, STEPS = BT / ROWS;
+  const int64_t n_q = static_cast<int64_t>(a.tiles) * a.Hq;
+  const bool on_v = NORMS && blockIdx.x >= n_q;
+  const int64_t at = on_v ? blockIdx.x - n_q : blockIdx.x;
+  const int H = on_v ? a.Hkv : a.Hq;
+  const Item it = a.items[at / H];
+  const int head = static_cast<int>(at % H);
+  const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+  const uint32_t mask = ((1u << LPR) - 1u) << ((threadIdx.x & 31) - l);
+  const Out& x = on_v ? a.v : a.dout;
+  uint4 xr[STEPS], yr[STEPS];
+  float dot[STEPS];
+  float most = 0.0f;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int i = row_index(it, it.tile, r0 + s * ROWS);
+    xr[s] = yr[s] = make_uint4(0, 0, 0, 0);
+    if (i < 0) continue;
+    const int64_t row = static_cast<int64_t>(it.start) + i;
+    xr[s] = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(x.ptr) + row * x.ts +
+                                            head * x.hs + 8 * l);
+    if (!on_v)
+      yr[s] = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.o.ptr) + row * a.o.ts +
+                                              head * a.o.hs + 8 * l);
+  }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    float f[8], g[8];
+    Cvt<T>::load8(xr[s], f);
+    Cvt<T>::load8(yr[s], g);
+    float p = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      p = fmaf(f[e], g[e], p);
+      if (NORMS) q = fmaf(f[e], f[e], q);
+    }
+    dot[s] = row_sum<LPR>(p, mask);
+    if (NORMS) {
+      q = row_sum<LPR>(q, mask);
+      most = q > most || q != q ? q : most;  // a NaN stays
+    }
+    const int i = row_index(it, it.tile, r0 + s * ROWS);
+    if (!on_v && l == 0 && i >= 0) a.dvec[head * a.T + it.start + i] = dot[s];
+  }
+  if (NORMS) {
+    // float bits of non-negative values (and NaN above all) order like unsigned integers, and a
+    // maximum does not depend on the order
+    uint32_t m = __float_as_uint(most) & 0x7fffffffu;
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) {
+      const int kv = on_v ? head : head / a.group;
+      atomicMax(&a.norms[(static_cast<int64_t>(it.seq) * a.Hkv + kv) * 2 + (on_v ? 1 : 0)], m);
+    }
+  }
+}
+
+// The factor of dS (a power of two) from the two norms; 1 where they say nothing.
+__device__ __forceinline__ float ds_factor(const uint32_t* norms) {
+  const float b = 2.0f * sqrtf(__uint_as_float(norms[0])) * sqrtf(__uint_as_float(norms[1]));
+  if (!(b > 0.0f) || b > 3.0e38f) return 1.0f;
+  int e = 14 - ilogbf(b);  // b 2^e in [2^14, 2^15)
+  e = max(-60, min(60, e));
+  return scalbnf(1.0f, e);
+}
+
+struct Args {
+  const Item* items;
+  const float* lse;   // [Hq][T]
+  const float* dvec;  // [Hq][T]
+  const uint32_t* norms;
+  Out out[2];         // dq_kernel: dq; dkv_kernel: dv, dk
+  int64_t T;
+  int heads;          // heads of the grid: query heads (dq), key heads (dkv)
+  int group;
+  int causal;
+  float scale_log2, tau;
+};
+
+// P (times 2^shift) of 64 columns from the scores x, in place: z = x c - shift(e).
+// MASK: columns for which hidden(e) holds are zero.
+template <bool MASK, typename Shift, typename Hidden>
+__device__ __forceinline__ void probabilities(uint32_t (&x)[2][32], float c, Shift shift,
+                                              Hidden hidden) {
+  const float2 c2 = make_float2(c, c);
+#pragma unroll
+  for (int e = 0; e < 64; e += 2) {
+    uint32_t& x0 = x[e >> 5][e & 31];
+    uint32_t& x1 = x[e >> 5][(e & 31) + 1];
+    float2 z = __ffma2_rn(make_float2(__uint_as_float(x0), __uint_as_float(x1)), c2, shift(e));
+    float2 p;
+    if (MASK) {
+      if (hidden(e)) z.x = -INFINITY;
+      if (hidden(e + 1)) z.y = -INFINITY;
+      p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+    } else if ((e & 7) == 6) {
+      p = exp2_fma2(z);
+    } else {
+      p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+    }
+    x0 = __float_as_uint(p.x);
+    x1 = __float_as_uint(p.y);
+  }
+}
+
+// ---- dK and dV ------------------------------------------------------------------------------
+template <typename T, int D>
+struct DkvSmem {
+  static constexpr int NST = D == 128 ? 4 : 8;  // Q / dO tiles in flight
+  alignas(1024) T k[BT * D];
+  alignas(1024) T v[BT * D];
+  alignas(1024) T ring[NST][BT * D];
+  alignas(16) float lse[2][BT];   // LSE log2 e - P's shift of the query tile's rows, +inf: padding
+  alignas(16) float dvec[2][BT];
+  uint64_t kv_full, full[NST], empty[NST], vec_full[2], vec_empty[2];
+  uint64_t s_full, dp_full, p_ready, ds_ready, done;
+  uint32_t tmem_base;
+  int abort;
+};
+template <typename T, int D>
+constexpr size_t dkv_smem_bytes() {
+  return sizeof(DkvSmem<T, D>) + 1024;
+}
+static_assert(dkv_smem_bytes<__half, 128>() <= 232448, "shared memory exceeds the limit");
+
+// TMEM columns: S^T (then P^T), dP^T (then dS^T), dV, dK.  P^T and dS^T of column half h start
+// at 64 h of their tile, over columns that only the same warps have read.
+constexpr uint32_t kColDP = 128, kColDV = 256, kColDK = 384;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+               const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  using SM = DkvSmem<T, D>;
+  SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  constexpr int NST = SM::NST;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Item it = a.items[blockIdx.x / a.heads];
+  const int kv_head = blockIdx.x % a.heads;
+  const int tiles = tiles_of(it);
+  // under a causal mask the list's order (most work first) is by query tile: mirrored for keys
+  const int kt = a.causal ? tiles - 1 - it.tile : it.tile;
+  const int first = a.causal ? kt : 0;          // first query tile that sees these keys
+  const int per_head = tiles - first;
+  const int n_all = per_head * a.group;
+  auto head_of = [&](int n) { return kv_head * a.group + n / per_head; };
+  auto tile_of = [&](int n) { return first + n % per_head; };
+
+  if (threadIdx.x == 0) {
+    sm.abort = device_aborted() ? 1 : 0;
+    mbar_init(&sm.kv_full, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.vec_full[s], 32);
+      mbar_init(&sm.vec_empty[s], 256);
+    }
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.dp_full, 1);
+    mbar_init(&sm.p_ready, 256);
+    mbar_init(&sm.ds_ready, 256);
+    mbar_init(&sm.done, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (sm.abort) return;
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    if (warp == kProducerWarp) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sm.kv_full, 2 * BT * D * 2);
+        load_tile<T, D>(sm.k, &tm_k, tile_at(it, kt), kv_head, &sm.kv_full);
+        load_tile<T, D>(sm.v, &tm_v, tile_at(it, kt), kv_head, &sm.kv_full);
+        for (int i = 0; i < 2 * n_all; ++i) {  // Q0 dO0 Q1 dO1 ...
+          const int st = i % NST, n = i >> 1;
+          if (i >= NST) mbar_wait(&sm.empty[st], ((i / NST) - 1) & 1, 401);
+          mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
+          load_tile<T, D>(sm.ring[st], (i & 1) ? &tm_do : &tm_q, tile_at(it, tile_of(n)),
+                          head_of(n), &sm.full[st]);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kRowWarp) {
+      for (int n = 0; n < n_all; ++n) {
+        const int b = n & 1;
+        if (n >= 2) mbar_wait(&sm.vec_empty[b], ((n >> 1) - 1) & 1, 402);
+        const int64_t base = head_of(n) * a.T + it.start;
+#pragma unroll
+        for (int r = lane; r < BT; r += 32) {
+          const int i = row_index(it, tile_of(n), r);
+          sm.lse[b][r] = i >= 0 ? fmaf(a.lse[base + i], kLog2e, -Scaling<T>::kPShift) : INFINITY;
+          sm.dvec[b][r] = i >= 0 ? a.dvec[base + i] : 0.0f;
+        }
+        mbar_arrive(&sm.vec_full[b]);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) {
+        constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+        constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
+        constexpr uint32_t id_g = instr_desc(1, kFmt, kFmt, false, true, BT, D);
+        const uint32_t ka = smem_u32(sm.k), va = smem_u32(sm.v);
+        auto wait_tile = [&](int i) { mbar_wait(&sm.full[i % NST], (i / NST) & 1, 411); };
+        auto product = [&](uint32_t col, uint32_t rows, int i, uint64_t* bar) {
+          wait_tile(i);
+          tc_fence_after();
+          const uint32_t b = smem_u32(sm.ring[i % NST]);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16(tmem + col, desc_k(rows, kk), desc_k(b, kk), id_s, kk > 0 ? 1u : 0u);
+          mma_commit(bar);
+        };
+        auto accumulate = [&](uint32_t col, uint32_t from, int i, bool start) {
+          const uint32_t b = smem_u32(sm.ring[i % NST]);
+#pragma unroll
+          for (int kk = 0; kk < BT / 16; ++kk)
+            mma_f16_ts(tmem + col, tmem + from + 64 * (kk >> 2) + 8 * (kk & 3), desc_mn(b, kk),
+                       id_g, (!start || kk > 0) ? 1u : 0u);
+          mma_commit(&sm.empty[i % NST]);
+        };
+        mbar_wait(&sm.kv_full, 0, 410);
+        product(0, ka, 0, &sm.s_full);
+        product(kColDP, va, 1, &sm.dp_full);
+        for (int n = 0; n < n_all; ++n) {
+          mbar_wait(&sm.p_ready, n & 1, 412);
+          tc_fence_after();
+          accumulate(kColDV, 0, 2 * n + 1, n == 0);  // dV += P^T dO
+          if (n + 1 < n_all) product(0, ka, 2 * n + 2, &sm.s_full);
+          mbar_wait(&sm.ds_ready, n & 1, 413);
+          tc_fence_after();
+          accumulate(kColDK, kColDP, 2 * n, n == 0);  // dK += dS^T Q
+          if (n + 1 < n_all) product(kColDP, va, 2 * n + 3, &sm.dp_full);
+        }
+        mma_commit(&sm.done);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    named_barrier_sync(15, kThreads);
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kComputeRegs));
+    const int half = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // key row of the tile
+    const uint32_t lane_base = tmem + (((warp & 3) * 32u) << 16);
+    const uint32_t s_at = lane_base + 64 * half, dp_at = s_at + kColDP;
+    const float c = a.scale_log2;
+    float factor = 1.0f;  // dS's factor over P's
+    if (Scaling<T>::kOn)
+      factor = ds_factor(a.norms + (static_cast<int64_t>(it.seq) * a.heads + kv_head) * 2);
+    const float f_ds = factor * exp2f(-Scaling<T>::kPShift);
+
+    auto step = [&](int n, auto masked) {
+      constexpr bool MASK = decltype(masked)::value;
+      const int b = n & 1;
+      uint32_t x[2][32];
+      mbar_wait(&sm.vec_full[b], (n >> 1) & 1, 420);
+      mbar_wait(&sm.s_full, n & 1, 421);
+      tc_fence_after();
+      tmem_ld32(s_at, x[0]);
+      tmem_ld32(s_at + 32, x[1]);
+      tmem_ld_wait_regs32(x[0]);
+      tie32(x[1]);
+      const float* lse = sm.lse[b] + 64 * half;
+      // query column below the key row's own position: hidden (diagonal tile of a causal mask)
+      probabilities<MASK>(
+          x, c,
+          [&](int e) {
+            const float2 s = *reinterpret_cast<const float2*>(lse + e);
+            return make_float2(-s.x, -s.y);
+          },
+          [&](int e) { return 64 * half + e < r; });
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = Cvt<T>::pack2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1]));
+        tmem_st16(s_at + 16 * h, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sm.p_ready);
+      // dS = P (dP - D)
+      mbar_wait(&sm.dp_full, n & 1, 422);
+      tc_fence_after();
+      uint32_t y[2][32];
+      tmem_ld32(dp_at, y[0]);
+      tmem_ld32(dp_at + 32, y[1]);
+      tmem_ld_wait_regs32(y[0]);
+      tie32(y[1]);
+      const float* dv = sm.dvec[b] + 64 * half;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 d2 = *reinterpret_cast<const float2*>(dv + 32 * h + 2 * e);
+          float2 p = make_float2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1]));
+          if (Scaling<T>::kOn) p = __fmul2_rn(p, make_float2(f_ds, f_ds));
+          const float2 t =
+              __fadd2_rn(make_float2(__uint_as_float(y[h][2 * e]),
+                                     __uint_as_float(y[h][2 * e + 1])),
+                         make_float2(-d2.x, -d2.y));
+          const float2 s = __fmul2_rn(p, t);
+          w[e] = Cvt<T>::pack2(s.x, s.y);
+        }
+        tmem_st16(dp_at + 16 * h, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sm.ds_ready);
+      mbar_arrive(&sm.vec_empty[b]);
+    };
+    for (int n = 0; n < n_all; ++n) {
+      if (a.causal && tile_of(n) == kt)
+        step(n, std::true_type{});
+      else
+        step(n, std::false_type{});
+    }
+    mbar_wait(&sm.done, 0, 423);
+    tc_fence_after();
+    // warps 0-3 store dV, warps 4-7 dK
+    const int i = row_index(it, kt, r);
+    const uint32_t g_at = lane_base + (half == 0 ? kColDV : kColDK);
+    const float scale = half == 0 ? exp2f(-Scaling<T>::kPShift) : a.tau / factor;
+    const Out& out = a.out[half];
+    T* dst = reinterpret_cast<T*>(out.ptr) + (static_cast<int64_t>(it.start) + i) * out.ts +
+             kv_head * out.hs;
+#pragma unroll
+    for (int cc = 0; cc < D; cc += 32) {
+      uint32_t y[32];
+      tmem_ld32(g_at + cc, y);
+      tmem_ld_wait_regs32(y);
+      if (i >= 0) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * scale;
+          *reinterpret_cast<uint4*>(dst + cc + e) = pack8<T>(f);
+        }
+      }
+    }
+    tc_fence_before();
+    named_barrier_sync(15, kThreads);
+  }
+}
+
+// ---- dQ -------------------------------------------------------------------------------------
+template <typename T, int D>
+struct DqSmem {
+  static constexpr int NST = D == 128 ? 5 : 8;  // K / V tiles in flight
+  alignas(1024) T q[BT * D];
+  alignas(1024) T dout[BT * D];
+  alignas(1024) T ring[NST][BT * D];
+  uint64_t q_full, full[NST], empty[NST], s_full[2], dp_full, dp_free, ds_ready, done;
+  uint32_t tmem_base;
+  int abort;
+};
+template <typename T, int D>
+constexpr size_t dq_smem_bytes() {
+  return sizeof(DqSmem<T, D>) + 1024;
+}
+static_assert(dq_smem_bytes<__half, 128>() <= 232448, "shared memory exceeds the limit");
+
+// TMEM columns: two S tiles (dS overwrites the one it came from) at 0 and 128, dP, dQ.
+constexpr uint32_t kColQdP = 256, kColQdQ = 384;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+              const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  using SM = DqSmem<T, D>;
+  SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  constexpr int NST = SM::NST;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Item it = a.items[blockIdx.x / a.heads];
+  const int head = blockIdx.x % a.heads;
+  const int kv_head = head / a.group;
+  const int tiles = tiles_of(it);
+  const int n_all = a.causal ? it.tile + 1 : tiles;
+
+  if (threadIdx.x == 0) {
+    sm.abort = device_aborted() ? 1 : 0;
+    mbar_init(&sm.q_full, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    mbar_init(&sm.s_full[0], 1);
+    mbar_init(&sm.s_full[1], 1);
+    mbar_init(&sm.dp_full, 1);
+    mbar_init(&sm.dp_free, 256);
+    mbar_init(&sm.ds_ready, 256);
+    mbar_init(&sm.done, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (sm.abort) return;
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    if (warp == kProducerWarp) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sm.q_full, 2 * BT * D * 2);
+        load_tile<T, D>(sm.q, &tm_q, tile_at(it, it.tile), head, &sm.q_full);
+        load_tile<T, D>(sm.dout, &tm_do, tile_at(it, it.tile), head, &sm.q_full);
+        for (int i = 0; i < 2 * n_all; ++i) {  // K0 V0 K1 V1 ...
+          const int st = i % NST;
+          if (i >= NST) mbar_wait(&sm.empty[st], ((i / NST) - 1) & 1, 501);
+          mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
+          load_tile<T, D>(sm.ring[st], (i & 1) ? &tm_v : &tm_k, tile_at(it, i >> 1), kv_head,
+                          &sm.full[st]);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) {
+        constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+        constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
+        constexpr uint32_t id_g = instr_desc(1, kFmt, kFmt, false, true, BT, D);
+        const uint32_t qa = smem_u32(sm.q), ga = smem_u32(sm.dout);
+        auto product = [&](uint32_t col, uint32_t rows, int i, uint64_t* bar) {
+          mbar_wait(&sm.full[i % NST], (i / NST) & 1, 511);
+          tc_fence_after();
+          const uint32_t b = smem_u32(sm.ring[i % NST]);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16(tmem + col, desc_k(rows, kk), desc_k(b, kk), id_s, kk > 0 ? 1u : 0u);
+          mma_commit(bar);
+        };
+        mbar_wait(&sm.q_full, 0, 510);
+        product(0, qa, 0, &sm.s_full[0]);
+        product(kColQdP, ga, 1, &sm.dp_full);
+        mma_commit(&sm.empty[1 % NST]);
+        if (n_all > 1) product(128, qa, 2, &sm.s_full[1]);
+        for (int j = 0; j < n_all; ++j) {
+          if (j + 1 < n_all) {  // dP of the next key tile once this one's has been read
+            mbar_wait(&sm.dp_free, j & 1, 512);
+            tc_fence_after();
+            product(kColQdP, ga, 2 * j + 3, &sm.dp_full);
+            mma_commit(&sm.empty[(2 * j + 3) % NST]);
+          }
+          mbar_wait(&sm.ds_ready, j & 1, 513);
+          tc_fence_after();
+          const uint32_t b = smem_u32(sm.ring[(2 * j) % NST]);
+#pragma unroll
+          for (int kk = 0; kk < BT / 16; ++kk)  // dQ += dS K
+            mma_f16_ts(tmem + kColQdQ, tmem + 128 * (j & 1) + 64 * (kk >> 2) + 8 * (kk & 3),
+                       desc_mn(b, kk), id_g, (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&sm.empty[(2 * j) % NST]);
+          if (j + 2 < n_all) product(128 * (j & 1), qa, 2 * j + 4, &sm.s_full[j & 1]);
+        }
+        mma_commit(&sm.done);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    named_barrier_sync(15, kThreads);
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kComputeRegs));
+    const int half = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // query row of the tile
+    const uint32_t lane_base = tmem + (((warp & 3) * 32u) << 16);
+    const int i = row_index(it, it.tile, r);
+    const int64_t row = static_cast<int64_t>(it.start) + i;
+    // padding rows: P = exp2(-inf) = 0
+    const float shift =
+        i >= 0 ? fmaf(a.lse[head * a.T + row], kLog2e, -Scaling<T>::kPShift) : INFINITY;
+    const float dvec = i >= 0 ? a.dvec[head * a.T + row] : 0.0f;
+    const float c = a.scale_log2;
+    float factor = 1.0f;
+    if (Scaling<T>::kOn)
+      factor = ds_factor(
+          a.norms + (static_cast<int64_t>(it.seq) * (a.heads / a.group) + kv_head) * 2);
+    const float f_ds = factor * exp2f(-Scaling<T>::kPShift);
+
+    auto step = [&](int j, auto masked) {
+      constexpr bool MASK = decltype(masked)::value;
+      const uint32_t s_at = lane_base + 128 * (j & 1) + 64 * half;
+      const uint32_t dp_at = lane_base + kColQdP + 64 * half;
+      uint32_t x[2][32];
+      mbar_wait(&sm.s_full[j & 1], (j >> 1) & 1, 520);
+      tc_fence_after();
+      tmem_ld32(s_at, x[0]);
+      tmem_ld32(s_at + 32, x[1]);
+      tmem_ld_wait_regs32(x[0]);
+      tie32(x[1]);
+      const int key0 = row_index(it, j, 64 * half);
+      const int last = a.causal ? i : 0x7fffffff;
+      probabilities<MASK>(
+          x, c, [&](int) { return make_float2(-shift, -shift); },
+          [&](int e) { return key0 + e < 0 || key0 + e > last; });
+      mbar_wait(&sm.dp_full, j & 1, 521);
+      tc_fence_after();
+      uint32_t y[2][32];
+      tmem_ld32(dp_at, y[0]);
+      tmem_ld32(dp_at + 32, y[1]);
+      tmem_ld_wait_regs32(y[0]);
+      tie32(y[1]);
+      tc_fence_before();
+      mbar_arrive(&sm.dp_free);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float2 p = make_float2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1]));
+          if (Scaling<T>::kOn) p = __fmul2_rn(p, make_float2(f_ds, f_ds));
+          const float2 t = __fadd2_rn(make_float2(__uint_as_float(y[h][2 * e]),
+                                                  __uint_as_float(y[h][2 * e + 1])),
+                                      make_float2(-dvec, -dvec));
+          const float2 s = __fmul2_rn(p, t);
+          w[e] = Cvt<T>::pack2(s.x, s.y);
+        }
+        tmem_st16(s_at + 16 * h, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sm.ds_ready);
+    };
+    const bool ragged = tiles * BT != it.len;
+    for (int j = 0; j < n_all; ++j) {
+      if ((j == 0 && ragged) || (a.causal && j == it.tile))
+        step(j, std::true_type{});
+      else
+        step(j, std::false_type{});
+    }
+    mbar_wait(&sm.done, 0, 522);
+    tc_fence_after();
+    // warps 0-3 store the first half of the channels, warps 4-7 the second
+    const float scale = a.tau / factor;
+    T* dst = reinterpret_cast<T*>(a.out[0].ptr) + row * a.out[0].ts + head * a.out[0].hs;
+#pragma unroll
+    for (int cc = half * (D / 2); cc < (half + 1) * (D / 2); cc += 32) {
+      uint32_t y[32];
+      tmem_ld32(lane_base + kColQdQ + cc, y);
+      tmem_ld_wait_regs32(y);
+      if (i >= 0) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * scale;
+          *reinterpret_cast<uint4*>(dst + cc + e) = pack8<T>(f);
+        }
+      }
+    }
+    tc_fence_before();
+    named_barrier_sync(15, kThreads);
+  }
+}
+
+}  // namespace bwd
+}  // namespace packed
+}  // namespace sage

@@ -1,0 +1,391 @@
+// packed_fwd.cuh -- 16-bit softmax attention over packed sequences with grouped heads, forward.
+//
+//   z_ij = tau q_i . k_j over the keys j of i's sequence (j <= i when causal)
+//   O_i = sum_j softmax(z_i)_j v_j,  LSE_i = log sum_j exp(z_ij)
+//
+// Tiles: a sequence of n tokens is cut into ceil(n / 128) tiles FROM ITS END, so only its
+// first tile is ragged, and query and key tiles share one alignment (the causal diagonal is the
+// diagonal of a tile).  The tiles are loaded through 4-D tensor maps (channel, row, token, head)
+// whose row and token axes have the same stride: the ragged tile starts at a negative row, which
+// the TMA unit reads as zeros, so no row of a neighbouring sequence ever enters shared memory
+// and non-finite values cannot leak through a product with a zero probability.
+//
+// Per CTA: two query tiles that share their keys: two heads of one group (an even number of
+// query heads per key head), else two neighbouring tiles of one head.
+//   warps 0-3, 4-7  softmax of tile 0 / 1, one query row per thread
+//   warp 8          TMA producer: the query tiles, then K and V tiles through a ring
+//   warp 9          MMA issuer: S = Q K^T (operands in shared memory), O += P V (P in TMEM)
+//   warps 10-11     idle (they complete the warpgroup that gives its registers away)
+// TMEM: S of tile g at 128 g (P overwrites its first 64 columns, two 16-bit values each), O of
+// tile g at 256 + 128 g, accumulated there over all keys.
+// The tensor core alternates between the tiles: while tile 0's softmax runs, it multiplies tile
+// 1's P V and Q K^T.  S of the next key tile is issued after P V of this one, so its arrival
+// also tells the softmax warps that O is up to date.
+// The running maximum that P is taken against is raised (and O rescaled in TMEM) only when a
+// row's maximum grows by more than 2^8: P then stays below 256, exact in the final division
+// by the row sum, and most key tiles leave O untouched.
+// Rounding: P to the tensors' type for P V (the sum l uses the unrounded P); O once at the end.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ptx.cuh"
+#include "rowops.cuh"
+
+namespace sage {
+namespace packed {
+
+constexpr int BT = 128;  // tokens per tile
+
+// One tile of a sequence (or the later of two neighbouring tiles).
+struct Item {
+  int start;  // first row of the sequence
+  int len;    // tokens of the sequence
+  int tile;   // tile index, 0 = the ragged one
+  int seq;    // sequence index
+};
+
+__host__ __device__ __forceinline__ int tiles_of(const Item& it) {
+  return static_cast<int>((static_cast<int64_t>(it.len) + BT - 1) / BT);
+}
+
+struct Out {
+  char* ptr;
+  int64_t ts, hs;  // elements
+};
+
+// Row and token coordinates of tile t in the 4-D maps.
+struct TileAt {
+  int row, token;
+};
+__device__ __forceinline__ TileAt tile_at(const Item& it, int t) {
+  const int pad = tiles_of(it) * BT - it.len;
+  TileAt a;
+  a.row = t == 0 ? -pad : 0;
+  a.token = it.start + (t == 0 ? 0 : t * BT - pad);
+  return a;
+}
+// Index within the sequence of row r of tile t (negative: padding).
+__device__ __forceinline__ int row_index(const Item& it, int t, int r) {
+  return (t - tiles_of(it)) * BT + it.len + r;
+}
+
+// Loads one tile of BT rows: D / 64 boxes of 64 channels (128-byte swizzled rows).
+template <typename T, int D>
+__device__ __forceinline__ void load_tile(T* dst, const CUtensorMap* map, TileAt at, int head,
+                                          uint64_t* bar) {
+#pragma unroll
+  for (int b = 0; b < D / 64; ++b)
+    tma_load_4d(dst + b * BT * 64, map, b * 64, at.row, at.token, head, bar);
+}
+
+// K-major operand: rows of a tile, K = 16 channels per step kk.
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk) {
+  return smem_desc(tile + (kk >> 2) * (BT * 128) + (kk & 3) * 32, 16, 1024, kSwizzle128B);
+}
+// MN-major operand: channels as N, 16 rows of the tile as K per step kk.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk) {
+  return smem_desc(tile + kk * 16 * 128, BT * 128, 1024, kSwizzle128B);
+}
+
+// 2^z for a pair as in exp2_poly2, for z <= 127 of unmasked scores: below 2^-126 the result is
+// 2^-126 instead of zero.
+__device__ __forceinline__ float2 exp2_fma2(float2 z) {
+  constexpr float kC0 = 1.0000001192092896f, kC1 = 0.6931469440460205f,
+                  kC2 = 0.24022120237350464f, kC3 = 0.05550713092088699f,
+                  kC4 = 0.009675540961325169f, kC5 = 0.0013276472454890609f;
+  const float2 zc = make_float2(fmaxf(z.x, -126.0f), fmaxf(z.y, -126.0f));
+  const float2 t = __fadd2_rn(zc, make_float2(kMagic, kMagic));
+  const float2 j = __fadd2_rn(t, make_float2(-kMagic, -kMagic));
+  const float2 f = __ffma2_rn(j, make_float2(-1.0f, -1.0f), zc);
+  float2 q = __ffma2_rn(make_float2(kC5, kC5), f, make_float2(kC4, kC4));
+  q = __ffma2_rn(q, f, make_float2(kC3, kC3));
+  q = __ffma2_rn(q, f, make_float2(kC2, kC2));
+  q = __ffma2_rn(q, f, make_float2(kC1, kC1));
+  q = __ffma2_rn(q, f, make_float2(kC0, kC0));
+  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
+}
+
+namespace fwd {
+
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 232, kOtherRegs = 40;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr uint32_t kColO = 256;
+
+template <typename T, int D>
+struct Smem {
+  static constexpr int NST = D == 128 ? 5 : 8;  // K / V tiles in flight
+  alignas(1024) T q[2][BT * D];
+  alignas(1024) T kv[NST][BT * D];
+  uint64_t q_full, full[NST], empty[NST], s_full[2], p_full[2], o_full;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <typename T, int D>
+constexpr size_t smem_bytes() {
+  return sizeof(Smem<T, D>) + 1024;
+}
+static_assert(smem_bytes<__half, 128>() <= 232448, "shared memory exceeds the limit");
+
+struct Args {
+  const Item* items;
+  Out o;
+  float* lse;  // [Hq][T]
+  int64_t T;
+  int head_groups;  // CTAs per item
+  int group;        // query heads per key head
+  int causal;
+  float scale_log2;  // softmax_scale log2(e)
+};
+
+// HEADS: the CTA's tiles are two heads of one group; otherwise tiles `tile` and `tile - 1` of one
+// head (the second absent when tile = 0).
+template <typename T, int D, bool HEADS>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  using SM = Smem<T, D>;
+  SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  constexpr int NST = SM::NST;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Item it = a.items[blockIdx.x / a.head_groups];
+  const int hg = blockIdx.x % a.head_groups;
+  const int head0 = HEADS ? 2 * hg : hg;
+  const int kv_head = head0 / a.group;
+  const bool two = HEADS || it.tile > 0;
+  auto tile_of = [&](int g) { return HEADS ? it.tile : it.tile - g; };
+  auto keys_of = [&](int g) { return a.causal ? tile_of(g) + 1 : tiles_of(it); };
+  const int n0 = keys_of(0);  // the most key tiles of the two
+  const int n1 = two ? keys_of(1) : 0;
+
+  if (threadIdx.x == 0) {
+    sm.abort = device_aborted() ? 1 : 0;
+    mbar_init(&sm.q_full, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&sm.s_full[g], 1);
+      mbar_init(&sm.p_full[g], 128);
+    }
+    mbar_init(&sm.o_full, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (sm.abort) return;
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    if (warp == kProducerWarp) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sm.q_full, (two ? 2 : 1) * BT * D * 2);
+        load_tile<T, D>(sm.q[0], &tm_q, tile_at(it, tile_of(0)), head0, &sm.q_full);
+        if (two)
+          load_tile<T, D>(sm.q[1], &tm_q, tile_at(it, tile_of(1)), HEADS ? head0 + 1 : head0,
+                          &sm.q_full);
+        for (int i = 0; i < 2 * n0; ++i) {  // K0 V0 K1 V1 ...
+          const int st = i % NST;
+          if (i >= NST) mbar_wait(&sm.empty[st], ((i / NST) - 1) & 1, 301);
+          mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
+          load_tile<T, D>(sm.kv[st], (i & 1) ? &tm_v : &tm_k, tile_at(it, i >> 1), kv_head,
+                          &sm.full[st]);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) {
+        constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+        constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
+        constexpr uint32_t id_o = instr_desc(1, kFmt, kFmt, false, true, BT, D);
+        auto scores = [&](int g, int j) {  // S_g = Q_g K_j^T
+          const uint32_t qa = smem_u32(sm.q[g]), ka = smem_u32(sm.kv[(2 * j) % NST]);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16(tmem + 128 * g, desc_k(qa, kk), desc_k(ka, kk), id_s, kk > 0 ? 1u : 0u);
+          mma_commit(&sm.s_full[g]);
+        };
+        auto wait_tile = [&](int i) { mbar_wait(&sm.full[i % NST], (i / NST) & 1, 311); };
+        mbar_wait(&sm.q_full, 0, 310);
+        wait_tile(0);
+        tc_fence_after();
+        scores(0, 0);
+        if (n1 > 0) scores(1, 0);
+        mma_commit(&sm.empty[0]);
+        for (int j = 0; j < n0; ++j) {
+          wait_tile(2 * j + 1);
+          if (j + 1 < n0) wait_tile(2 * j + 2);
+          const uint32_t va = smem_u32(sm.kv[(2 * j + 1) % NST]);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int n = g == 0 ? n0 : n1;
+            if (j >= n) continue;
+            mbar_wait(&sm.p_full[g], j & 1, 312);
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < BT / 16; ++kk)
+              mma_f16_ts(tmem + kColO + 128 * g, tmem + 128 * g + 8 * kk, desc_mn(va, kk), id_o,
+                         (j > 0 || kk > 0) ? 1u : 0u);
+            if (j + 1 < n) scores(g, j + 1);
+          }
+          mma_commit(&sm.empty[(2 * j + 1) % NST]);
+          if (j + 1 < n0) mma_commit(&sm.empty[(2 * j + 2) % NST]);
+        }
+        mma_commit(&sm.o_full);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    named_barrier_sync(15, kThreads);
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    const int g = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + (((warp & 3) * 32u) << 16);
+    const uint32_t s_at = lane_base + 128 * g, o_at = lane_base + kColO + 128 * g;
+    const int n = g == 0 ? n0 : n1;
+    const int tile = tile_of(g);
+    const int i = row_index(it, tile, r);
+    const float c = a.scale_log2;
+    float m = -INFINITY, l = 0.0f;
+
+    auto block = [&](int j, auto masked) {
+      constexpr bool MASK = decltype(masked)::value;
+      mbar_wait(&sm.s_full[g], j & 1, 320);
+      tc_fence_after();
+      uint32_t x[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(s_at + 32 * q, x[q]);
+      tmem_ld_wait_regs32(x[0]);
+      tie32(x[1]);
+      tie32(x[2]);
+      tie32(x[3]);
+      if (MASK) {
+        // key index within the sequence must be >= 0 (the ragged first tile) and, when causal,
+        // not above the row's
+        const int lo = -row_index(it, j, 0);
+        const int hi = a.causal ? i - row_index(it, j, 0) : BT - 1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * q + e < lo || 32 * q + e > hi) x[q][e] = 0xff800000u;  // -inf
+      }
+      float mx[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        mx[q] = fmaxf(__uint_as_float(x[q][0]), __uint_as_float(x[q][1]));
+#pragma unroll
+        for (int e = 2; e < 32; e += 2)
+          mx[q] = fmax3(mx[q], __uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      const bool grow = top > m + 8.0f;  // always on the first tile with a visible key
+      if (__any_sync(0xffffffffu, grow)) {
+        const float mn = grow ? top : m;
+        const float alpha = grow ? ex2_approx(m - mn) : 1.0f;
+        m = mn;
+        l *= alpha;
+        if (j > 0) {
+#pragma unroll
+          for (int cc = 0; cc < D; cc += 32) {
+            uint32_t y[32];
+            tmem_ld32(o_at + cc, y);
+            tmem_ld_wait_regs32(y);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+            tmem_st32(o_at + cc, y);
+          }
+        }
+      }
+      const float neg = m == -INFINITY ? 0.0f : -m;
+      const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
+      float2 sum = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const int q = 2 * hh + (e >> 5), ee = e & 31;
+          const float2 z = __ffma2_rn(
+              make_float2(__uint_as_float(x[q][ee]), __uint_as_float(x[q][ee + 1])), c2, n2);
+          float2 p;
+          if (!MASK && (e & 7) == 6)
+            p = exp2_fma2(z);
+          else
+            p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+          if (e & 2)
+            sum2 = __fadd2_rn(sum2, p);
+          else
+            sum = __fadd2_rn(sum, p);
+          w[e >> 1] = Cvt<T>::pack2(p.x, p.y);
+        }
+        tmem_st32(s_at + 32 * hh, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sm.p_full[g]);
+      l += (sum.x + sum.y) + (sum2.x + sum2.y);
+    };
+    const bool ragged = tiles_of(it) * BT != it.len;
+    for (int j = 0; j < n; ++j) {
+      if ((j == 0 && ragged) || (a.causal && j == tile))
+        block(j, std::true_type{});
+      else
+        block(j, std::false_type{});
+    }
+    mbar_wait(&sm.o_full, 0, 321);
+    tc_fence_after();
+    if (n > 0) {
+      const int head = HEADS ? head0 + g : head0;
+      const float inv_l = 1.0f / l;
+      const int64_t row = static_cast<int64_t>(it.start) + i;
+      T* out = reinterpret_cast<T*>(a.o.ptr) + row * a.o.ts + head * a.o.hs;
+#pragma unroll
+      for (int cc = 0; cc < D; cc += 32) {
+        uint32_t y[32];
+        tmem_ld32(o_at + cc, y);
+        tmem_ld_wait_regs32(y);
+        if (i >= 0) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * inv_l;
+            *reinterpret_cast<uint4*>(out + cc + e) = pack8<T>(f);
+          }
+        }
+      }
+      if (i >= 0) a.lse[head * a.T + row] = (m + log2f(l)) * 0.69314718055994531f;
+    }
+    tc_fence_before();
+    named_barrier_sync(15, kThreads);
+  }
+}
+
+}  // namespace fwd
+}  // namespace packed
+}  // namespace sage

@@ -1081,3 +1081,5 @@ int sage_kv_finalize(const sage_params* p, const void* k, const sage_qbufs* qb,
 }
 
 }  // extern "C"
+
+#include "packed_api.cuh"

@@ -1,0 +1,326 @@
+"""Packed grouped-head attention on the GPU against its 64-bit definition.
+
+Every comparison is element by element against a bound computed with the reference (packed_ref):
+one rounding of P, dS and each output to the 16-bit type, float32 sums.
+"""
+import math
+
+import pytest
+import torch
+
+import packed_ref as R
+from fwd_bwd_b200 import ops, packed
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+def _inputs(T, hq, hkv, d, dt, layout="fused", seed=0, do_scale=1e-2):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if layout == "fused":  # slices of one projection's output, with columns nobody reads
+        x = torch.randn((T, hq + 2 * hkv + 1, d), generator=g, device="cuda").to(dt)
+        q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:hq + 2 * hkv]
+    elif layout == "heads":  # [H, T, d] storage
+        q, k, v = (torch.randn((h, T, d), generator=g, device="cuda").to(dt).transpose(0, 1)
+                   for h in (hq, hkv, hkv))
+    else:
+        q, k, v = (torch.randn((T, h, d), generator=g, device="cuda").to(dt)
+                   for h in (hq, hkv, hkv))
+    do = (torch.randn((T, hq, d), generator=g, device="cuda") * do_scale).to(dt)
+    return q, k, v, do
+
+
+def _run(q, k, v, do, lengths, causal=True, scale=0.0):
+    b = packed.Batch(lengths)
+    o, lse = packed.attn_fwd(q, k, v, b, causal, scale)
+    dq, dk, dv = packed.attn_bwd(q, k, v, o, lse, do, b, causal, scale)
+    torch.cuda.synchronize()
+    assert ops.device_status() == 0
+    return {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
+
+
+def _check(got, q, k, v, do, lengths, causal=True, scale=0.0):
+    ref = R.attention(q, k, v, lengths, causal, scale or 1 / math.sqrt(q.shape[2]), do)
+    n = sum(lengths)
+    for name, x in got.items():
+        rows = (slice(None), slice(0, n)) if name == "lse" else slice(0, n)
+        part = {name: ref[name][rows], name + "_tol": ref[name + "_tol"][rows]}
+        R.close(x[rows], part, name)
+    return ref
+
+
+LENGTHS = [[1], [2], [127], [128], [129], [257], [1, 1, 1], [0, 5, 0, 131, 0],
+           [300, 5, 1, 128, 0, 777], [64] * 7, [1500, 3]]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lengths", LENGTHS, ids=lambda v: "-".join(map(str, v)))
+def test_lengths(lengths, causal):
+    q, k, v, do = _inputs(sum(lengths), 2, 1, 128, BF)
+    _check(_run(q, k, v, do, lengths, causal), q, k, v, do, lengths, causal)
+
+
+@pytest.mark.parametrize("layout", ["fused", "heads", "plain"])
+@pytest.mark.parametrize("heads", [(1, 1), (2, 1), (3, 1), (6, 2), (5, 5), (16, 2), (12, 4)],
+                         ids=str)
+@pytest.mark.parametrize("d,dt", [(64, BF), (64, HF), (128, BF), (128, HF)])
+def test_heads_types_layouts(heads, d, dt, layout):
+    lengths = [200, 1, 333, 0, 130]
+    q, k, v, do = _inputs(sum(lengths), *heads, d, dt, layout, seed=heads[0])
+    causal = (heads[0] + d // 64) % 2 == 0
+    _check(_run(q, k, v, do, lengths, causal), q, k, v, do, lengths, causal)
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_long_sequence(dt):
+    lengths = [4133, 900]
+    q, k, v, do = _inputs(sum(lengths), 4, 2, 128, dt, seed=5)
+    _check(_run(q, k, v, do, lengths), q, k, v, do, lengths)
+
+
+@pytest.mark.parametrize("d,dt,heads", [(64, HF, (4, 2)), (128, BF, (4, 2)), (128, BF, (3, 3))])
+def test_growing_maximum(d, dt, heads):
+    """Scores that rise along the sequence by hundreds: the running maximum is raised, and O
+    rescaled, on many key tiles; whole tiles' probabilities vanish."""
+    lengths = [1000, 513]
+    q, k, v, do = _inputs(sum(lengths), *heads, d, dt, "plain", seed=6)
+    ramp = torch.cat([torch.linspace(0.0, 6.0, n, device="cuda") for n in lengths])
+    q = (q * 4).contiguous()
+    k = (k * (0.2 + ramp[:, None, None])).to(dt)
+    for causal in (True, False):
+        _check(_run(q, k, v, do, lengths, causal), q, k, v, do, lengths, causal)
+
+
+@pytest.mark.parametrize("do_scale", [2.0 ** -18, 200.0])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_gradient_magnitudes(dt, do_scale):
+    """Small and large dO: half precision's dS would vanish or overflow without its factor.  dO
+    near half's smallest normal is itself coarse, but it is the input; what the outputs lose to
+    their own type's subnormals is in the bound."""
+    lengths = [513, 70]
+    q, k, v, do = _inputs(sum(lengths), 4, 2, 64, dt, seed=7, do_scale=do_scale)
+    _check(_run(q, k, v, do, lengths), q, k, v, do, lengths)
+
+
+def test_zero_gradient_and_zero_inputs():
+    lengths = [200, 31]
+    q, k, v, do = _inputs(sum(lengths), 2, 2, 64, HF)
+    got = _run(q, k, v, torch.zeros_like(do), lengths)
+    for n in ("dq", "dk", "dv"):
+        assert not got[n].any(), n
+    z = torch.zeros_like(k)
+    got = _run(q, z, z, do, lengths)  # uniform attention over zero values
+    assert not got["o"].any() and not got["dq"].any()
+    _check(got, q, z, z, do, lengths)
+
+
+@pytest.mark.parametrize("scale", [0.01, 0.5])
+def test_softmax_scale(scale):
+    lengths = [140, 9]
+    q, k, v, do = _inputs(sum(lengths), 2, 1, 64, BF)
+    _check(_run(q, k, v, do, lengths, True, scale), q, k, v, do, lengths, True, scale)
+
+
+@pytest.mark.parametrize("heads", [(2, 1), (1, 1)], ids=str)
+@pytest.mark.parametrize("causal", [True, False])
+def test_sequences_never_touch(causal, heads):
+    """NaN and infinity in some sequences and behind the last one: the others' results are bit
+    for bit those without them, and the rows behind the last stay as they were."""
+    lengths = [130, 77, 300, 1, 255]
+    n, extra = sum(lengths), 140
+    q, k, v, do = _inputs(n + extra, *heads, 128, HF, "plain", seed=8)
+    clean = _run(q, k, v, do, lengths, causal)
+    bad = [x.clone() for x in (q, k, v, do)]
+    at = 0
+    good = torch.zeros(n + extra, dtype=torch.bool, device="cuda")
+    for i, m in enumerate(lengths):
+        if i % 2 == 0:
+            good[at:at + m] = True
+        else:
+            for j, x in enumerate(bad):
+                x[at:at + m] = [math.nan, math.inf, -math.inf, math.nan][(i + j) % 4]
+        at += m
+    for x in bad:
+        x[n:] = math.nan
+    b = packed.Batch(lengths)
+    o = torch.full_like(q, 7.0)
+    lse = torch.full((heads[0], n + extra), 7.0, device="cuda")
+    grads = [torch.full_like(x, 7.0) for x in (q, k, v)]
+    packed.attn_fwd(*bad[:3], b, causal, o=o, lse=lse)
+    packed.attn_bwd(*bad[:3], o, lse, bad[3], b, causal, dq=grads[0], dk=grads[1], dv=grads[2])
+    torch.cuda.synchronize()
+    assert ops.device_status() == 0
+    for name, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse.t(), *grads)):
+        want = clean[name].t() if name == "lse" else clean[name]
+        assert torch.equal(x[good], want[good]), name
+        assert bool((x[n:] == 7.0).all()), name
+    for name, x in clean.items():  # new outputs: zero there
+        assert not (x[:, n:] if name == "lse" else x[n:]).any(), name
+
+
+def test_padded_rows_of_new_outputs_are_zero_in_autograd():
+    lengths = [100, 20]
+    q, k, v, _ = _inputs(150, 2, 1, 64, BF, "plain")
+    q, k, v = (x.clone().requires_grad_(True) for x in (q, k, v))
+    o = packed.packed_attention(q, k, v, packed.Batch(lengths))
+    o.sum().backward()  # the gradient is a broadcast scalar
+    for x in (q, k, v):
+        assert not x.grad[120:].any() and torch.isfinite(x.grad).all()
+
+
+def test_autograd_equals_the_calls():
+    lengths = [222, 90]
+    q, k, v, do = _inputs(sum(lengths), 4, 2, 128, BF, "fused")
+    got = _run(q, k, v, do, lengths)
+    leaves = [x.clone().requires_grad_(True) for x in (q, k, v)]
+    o = packed.packed_attention(*leaves, packed.Batch(lengths))
+    o.backward(do)
+    assert torch.equal(o, got["o"])
+    for x, n in zip(leaves, ("dq", "dk", "dv")):
+        assert torch.equal(x.grad, got[n]), n
+    # keys and values given once for all heads (a broadcast input): their gradients add up
+    k1 = k[:, :1].clone().requires_grad_(True)
+    o = packed.packed_attention(q, k1.expand(-1, 2, -1), v, packed.Batch(lengths))
+    o.backward(do)
+    kk = k[:, :1].expand(-1, 2, -1).contiguous()
+    want = _run(q, kk, v, do, lengths)["dk"]
+    assert torch.equal(k1.grad, want.sum(1, keepdim=True))
+
+
+def test_same_bits_every_time():
+    lengths = [700, 300, 45]
+    q, k, v, do = _inputs(sum(lengths), 8, 2, 128, BF, seed=9)
+    first = _run(q, k, v, do, lengths)
+    for _ in range(3):
+        again = _run(q, k, v, do, lengths)
+        for n in first:
+            assert torch.equal(first[n], again[n]), n
+
+
+def test_sequence_alone_equals_sequence_in_a_batch():
+    lengths = [129, 300, 64]
+    q, k, v, do = _inputs(sum(lengths), 6, 2, 64, BF, seed=10)
+    whole = _run(q, k, v, do, lengths)
+    at = 0
+    for n in lengths:
+        r = slice(at, at + n)
+        one = _run(q[r], k[r], v[r], do[r], [n])
+        for name in ("o", "dq", "dk", "dv"):
+            assert torch.equal(whole[name][r], one[name]), (n, name)
+        assert torch.equal(whole["lse"][:, r], one["lse"])
+        at += n
+
+
+def test_strided_outputs():
+    lengths = [150, 61]
+    T = sum(lengths)
+    q, k, v, do = _inputs(T, 4, 2, 64, BF)
+    want = _run(q, k, v, do, lengths)
+    b = packed.Batch(lengths)
+    fused = torch.zeros((T, 4 + 2 * 2, 64), dtype=BF, device="cuda")
+    o = torch.zeros((4, T, 64), dtype=BF, device="cuda").transpose(0, 1)
+    _, lse = packed.attn_fwd(q, k, v, b, o=o)
+    packed.attn_bwd(q, k, v, o, lse, do, b, dq=fused[:, :4], dk=fused[:, 4:6], dv=fused[:, 6:])
+    assert torch.equal(o, want["o"])
+    assert torch.equal(fused, torch.cat([want["dq"], want["dk"], want["dv"]], 1))
+
+
+def test_side_stream_and_graph():
+    lengths = [333, 128, 7]
+    q, k, v, do = _inputs(sum(lengths), 4, 2, 64, HF, "plain", seed=11)
+    b = packed.Batch(lengths)
+    want = _run(q, k, v, do, lengths)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o, lse = packed.attn_fwd(q, k, v, b)
+        grads = packed.attn_bwd(q, k, v, o, lse, do, b)
+    side.synchronize()
+    for n, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+        assert torch.equal(x, want[n]), n
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = packed.attn_fwd(q, k, v, b)
+        grads = packed.attn_bwd(q, k, v, o, lse, do, b)
+    for seed in (11, 12, 13):
+        for x, y in zip((q, k, v, do), _inputs(sum(lengths), 4, 2, 64, HF, "plain", seed=seed)):
+            x.copy_(y)
+        for x in (o, lse, *grads):
+            x.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ops.device_status() == 0
+        want = _run(q, k, v, do, lengths)
+        for n, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+            assert torch.equal(x, want[n]), (seed, n)
+
+
+def test_backward_captured_beside_a_live_eager_graph():
+    lengths = [90, 40]
+    q, k, v, do = _inputs(sum(lengths), 2, 1, 64, BF, "plain")
+    b = packed.Batch(lengths)
+    leaves = [x.clone().requires_grad_(True) for x in (q, k, v)]
+    eager = packed.packed_attention(*leaves, b)  # its graph stays alive over the capture
+    graph = torch.cuda.CUDAGraph()
+    copies = [x.detach().clone().requires_grad_(True) for x in leaves]
+    with torch.cuda.graph(graph):
+        o = packed.packed_attention(*copies, b)
+        grads = torch.autograd.grad(o, copies, do)
+    graph.replay()
+    eager.backward(do)
+    torch.cuda.synchronize()
+    for x, g in zip(leaves, grads):
+        assert torch.equal(x.grad, g)
+
+
+def test_rows_past_2_31_elements():
+    """Offsets beyond 32 bits: the last sequence's rows lie past 2^32 bytes and 2^31 elements."""
+    hq, d = 2, 64
+    stride = 1 << 21  # elements from token to token
+    T = 1100
+    store = torch.empty((T, stride), dtype=BF, device="cuda")
+    small = _inputs(T, hq, 1, d, BF, "plain", seed=14)
+    q = store[:, :hq * d].unflatten(1, (hq, d))
+    k = store[:, 1024:1024 + d].unflatten(1, (1, d))
+    v = store[:, 2048:2048 + d].unflatten(1, (1, d))
+    for x, y in zip((q, k, v), small):
+        x.copy_(y)
+    lengths = [1000, 100]
+    want = _run(*small, lengths)
+    o = store[:, 4096:4096 + hq * d].unflatten(1, (hq, d))
+    b = packed.Batch(lengths)
+    _, lse = packed.attn_fwd(q, k, v, b, o=o)
+    dq, dk, dv = packed.attn_bwd(q, k, v, o, lse, small[3], b)
+    for n, x in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        assert torch.equal(x, want[n]), n
+
+
+def test_refusals_on_device_tensors():
+    q, k, v, do = _inputs(10, 4, 2, 64, BF, "plain")
+    b = packed.Batch([10])
+    ok = lambda **kw: packed.attn_fwd(**{**dict(q=q, k=k, v=v, batch=b), **kw})  # noqa: E731
+    o, lse = ok()
+    cases = [dict(q=q.float()), dict(q=q.cpu()), dict(q=q[:, :3]), dict(k=k[:9]), dict(v=v[:, :1]),
+             dict(q=q[..., :32]), dict(v=v.to(HF)), dict(batch=packed.Batch([11])),
+             dict(batch=packed.Batch([10], device="cpu")), dict(q=q[0]),
+             dict(k=k[:, :1].expand(-1, 2, -1)), dict(o=o[:, :2]), dict(lse=lse.t()),
+             dict(q=q.transpose(1, 2).contiguous().transpose(1, 2))]
+    for kw in cases:
+        with pytest.raises((ValueError, RuntimeError)):
+            ok(**kw)
+    overlap = torch.zeros((10, 64 * 2), dtype=BF, device="cuda").as_strided((10, 4, 64), (64, 64, 1))
+    with pytest.raises(RuntimeError, match="INVALID_ARG"):
+        ok(o=overlap)
+    with pytest.raises(RuntimeError, match="INVALID_ARG"):
+        ok(softmax_scale=math.inf)
+    with pytest.raises(RuntimeError, match="WORKSPACE"):
+        packed.attn_bwd(q, k, v, o, lse, do, b,
+                        workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert packed.workspace_bytes(q, k, v, b) >= 4 * 10 * 4
+
+
+def test_only_empty_sequences():
+    q, k, v, do = _inputs(5, 2, 1, 64, BF, "plain")
+    got = _run(q, k, v, do, [0, 0])
+    assert not any(x.any() for x in got.values())
