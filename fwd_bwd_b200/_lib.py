@@ -60,7 +60,8 @@ class SageRopeParams(ctypes.Structure):
 
 class SagePackedInfo(ctypes.Structure):
     _fields_ = [("sequences", ctypes.c_int), ("tiles", ctypes.c_int), ("pairs", ctypes.c_int),
-                ("longest", ctypes.c_int), ("tokens", ctypes.c_int64)]
+                ("longest", ctypes.c_int), ("tokens", ctypes.c_int64),
+                ("causal_steps", ctypes.c_int64), ("full_steps", ctypes.c_int64)]
 
 
 class SagePackedParams(ctypes.Structure):

@@ -78,10 +78,6 @@ uint64_t turn_fraction(double inv_freq) {
   return scaled >= 18446744073709551615.0L ? 0 : static_cast<uint64_t>(scaled + 0.5L);
 }
 
-sage::rope::Rows rope_rows(const sage_rows* r) {
-  return {static_cast<char*>(r->ptr), r->batch_stride, r->token_stride, r->head_stride};
-}
-
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -90,62 +86,80 @@ int sm_count() {
   return n;
 }
 
-// Blocks of the gradient kernel at most: their partial sums of the gains' gradients are added
-// up by one small kernel, so their number is kept to four per SM of a 148-SM device.
-constexpr int kRopeBwdBlocks = 592;
+// Blocks of the gradient kernel at most (two per SM of a 148-SM device): their partial sums of
+// the gains' gradients are added up by one small kernel.
+constexpr int kRopeBwdBlocks = 296;
 
-void rope_args(const sage_rope_params* p, sage::rope::Args* a) {
+sage::rope::Rows rope_rows(const sage_rows* r) {
+  return {static_cast<char*>(r->ptr), r->batch_stride, r->token_stride, r->head_stride};
+}
+
+void rope_args(const sage_rope_params* p, const sage_rows* q, const sage_rows* k,
+               const sage_rows* yq, const sage_rows* yk, const float* gain_q,
+               const float* gain_k, const void* pos, sage::rope::Args* a) {
   std::memset(a, 0, sizeof(*a));
+  a->x[0] = rope_rows(q);
+  a->x[1] = rope_rows(k);
+  a->y[0] = rope_rows(yq);
+  a->y[1] = rope_rows(yk);
+  a->gain[0] = gain_q;
+  a->gain[1] = gain_k;
+  a->pos = pos;
   a->tokens = p->B * p->N;
   a->N = p->N;
   a->Hq = p->Hq;
-  a->Hkv = p->Hkv;
+  a->H = p->Hq + p->Hkv;
   a->rotary = p->rotary_dim;
-  a->interleaved = p->interleaved;
   a->norm = p->norm;
   a->eps = p->eps;
   for (int& b : a->bound) b = 64;  // beyond the last pair
   if (p->rotary_dim > 0) {
-    a->n_axes = p->n_axes;
     a->pos64 = p->pos_bits == 64;
     a->pos_as = p->pos_axis_stride;
     a->pos_bs = p->pos_batch_stride;
     for (int i = 0; i < p->rotary_dim / 2; ++i) a->freq[i] = turn_fraction(p->inv_freq[i]);
     for (int i = 0, at = 0; i + 1 < p->n_axes; ++i) a->bound[i] = at += p->sections[i];
   }
-  // Heads of a token per lane group: all of them when there are tokens enough to fill the
-  // device (the angles are then computed once per token), fewer otherwise.
-  const int H = p->Hq + p->Hkv;
-  const int want = 2 * 148 * 1024 / (p->d / 8);  // lane groups that keep the memory system busy
-  const int chunks = std::max(1, std::min(H, (want + a->tokens - 1) / a->tokens));
-  a->per_chunk = (H + chunks - 1) / chunks;
-  a->chunks = (H + a->per_chunk - 1) / a->per_chunk;
+  // Heads of a token per lane group: all of them when there are many times more tokens than
+  // groups on the device (the angles are then computed once per token), fewer otherwise; a
+  // multiple of the rows computed together.
+  const int64_t want = 2 * 148 * 1024 / (p->d / 8);  // two rounds of lane groups
+  const int64_t chunks = std::max<int64_t>(1, (want + a->tokens - 1) / a->tokens);
+  const int per = static_cast<int>(std::max<int64_t>(1, a->H / chunks));
+  a->per_chunk = per >= 4 ? per / 4 * 4 : per;
+  if (chunks == 1) a->per_chunk = a->H;
+  a->chunks = (a->H + a->per_chunk - 1) / a->per_chunk;
 }
 
-template <typename T, int D, bool BWD>
+template <typename T, int D, bool INTER, bool BWD>
 int run_rope(sage::rope::Args* a, float* dgain_q, float* dgain_k, cudaStream_t st) {
   const int groups = sage::rope::kThreads / (D / 8);
-  const int64_t units = static_cast<int64_t>(a->tokens) * a->chunks;
-  const int64_t need = (units + groups - 1) / groups;
   const int sms = sm_count();
   if (sms == 0) return SAGE_ERR_CUDA;
-  const int64_t most = BWD ? std::min(kRopeBwdBlocks, 4 * sms) : 8 * sms;
-  const int blocks = static_cast<int>(std::min(need, most));
-  sage::rope::qk_rope_kernel<T, D, BWD><<<blocks, sage::rope::kThreads, 0, st>>>(*a);
+  const int64_t need = static_cast<int64_t>((a->tokens + groups - 1) / groups) * a->chunks;
+  const int most = BWD ? std::min(kRopeBwdBlocks, 2 * sms) : 3 * sms;  // resident at once
+  const int blocks = static_cast<int>(std::min<int64_t>(need, most));
+  sage::rope::qk_rope_kernel<T, D, INTER, BWD><<<blocks, sage::rope::kThreads, 0, st>>>(*a);
   if (BWD && a->partial)
     sage::rope::dgain_kernel<D><<<2 * D / 32, 1024, 0, st>>>(a->partial, blocks, dgain_q, dgain_k);
   return launch_status();
 }
 
+template <bool BWD, typename T, int D>
+int run_rope(const sage_rope_params* p, sage::rope::Args* a, float* dgain_q, float* dgain_k,
+             cudaStream_t st) {
+  return p->interleaved ? run_rope<T, D, true, BWD>(a, dgain_q, dgain_k, st)
+                        : run_rope<T, D, false, BWD>(a, dgain_q, dgain_k, st);
+}
 template <bool BWD>
 int launch_rope(const sage_rope_params* p, sage::rope::Args* a, float* dgain_q, float* dgain_k,
                 cudaStream_t st) {
   const bool bf = p->dtype == SAGE_BF16;
   if (p->d == 128)
-    return bf ? run_rope<__nv_bfloat16, 128, BWD>(a, dgain_q, dgain_k, st)
-              : run_rope<__half, 128, BWD>(a, dgain_q, dgain_k, st);
-  return bf ? run_rope<__nv_bfloat16, 64, BWD>(a, dgain_q, dgain_k, st)
-            : run_rope<__half, 64, BWD>(a, dgain_q, dgain_k, st);
+    return bf ? run_rope<BWD, __nv_bfloat16, 128>(p, a, dgain_q, dgain_k, st)
+              : run_rope<BWD, __half, 128>(p, a, dgain_q, dgain_k, st);
+  return bf ? run_rope<BWD, __nv_bfloat16, 64>(p, a, dgain_q, dgain_k, st)
+            : run_rope<BWD, __half, 64>(p, a, dgain_q, dgain_k, st);
 }
 
 // ---- packed plan --------------------------------------------------------------------------
@@ -155,7 +169,7 @@ int launch_rope(const sage_rope_params* p, sage::rope::Args* a, float* dgain_q, 
 // (named by the later one, cut from the sequence's end) in the same two orders.
 bool plan_counts(const int* lengths, int n, sage_packed_info* info) {
   if (!lengths || n < 1) return false;
-  int64_t tokens = 0, tiles = 0, pairs = 0;
+  int64_t tokens = 0, tiles = 0, pairs = 0, causal = 0, full = 0;
   int longest = 0;
   for (int i = 0; i < n; ++i) {
     if (lengths[i] < 0) return false;
@@ -164,6 +178,8 @@ bool plan_counts(const int* lengths, int n, sage_packed_info* info) {
     const int64_t t = (static_cast<int64_t>(lengths[i]) + sage::packed::BT - 1) / sage::packed::BT;
     tiles += t;
     pairs += (t + 1) / 2;
+    causal += t * (t + 1) / 2;
+    full += t * t;
     longest = std::max(longest, lengths[i]);
   }
   info->sequences = n;
@@ -171,6 +187,8 @@ bool plan_counts(const int* lengths, int n, sage_packed_info* info) {
   info->pairs = static_cast<int>(pairs);
   info->longest = longest;
   info->tokens = tokens;
+  info->causal_steps = causal;
+  info->full_steps = full;
   return true;
 }
 
@@ -217,9 +235,20 @@ bool make_tile_map(CUtensorMap* m, const sage_rows* r, const sage_packed_params*
   cuuint64_t strides[3] = {ts * 2, ts * 2, hs * 2};
   cuuint32_t box[4] = {64, sage::packed::BT, 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, r->ptr, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&] {
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, r->ptr, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult s = encode();
+  if (s == CUDA_ERROR_INVALID_CONTEXT || s == CUDA_ERROR_NOT_INITIALIZED) {
+    // a host thread that has made no runtime call yet (autograd's, say) has no current context:
+    // bind the one of its current device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+    s = encode();
+  }
+  return s == CUDA_SUCCESS;
 }
 
 sage::packed::Out packed_out(const sage_rows* r) {
@@ -237,6 +266,22 @@ int launch_packed(K kern, int regs, int64_t grid, int threads, size_t smem, cuda
   return launch_status();
 }
 
+// Heads per chunk of the grid (packed::Grid) when the CTAs of one head read bytes_per_head over
+// and over: as many as kChunkBytes holds, so that they stay in L2 (B200, 16 heads, 4 x 8192 tokens,
+// d = 128: forward 1023 -> 933 us, dK/dV 1951 -> 1685 us, dQ 1649 -> 1365 us against all heads at
+// once); but at least so many that a chunk keeps the device busy for longer than its longest
+// item takes, because the last chunk's long items start late (16384 tokens in documents of
+// 5021 to 2, 4 key heads, dK/dV: 330 us in one chunk, 442 us in four).
+constexpr int64_t kChunkBytes = 40 << 20;  // of the 126 MB L2
+int grid_chunk(const sage_packed_params* p, const sage_packed_info* info, int heads,
+               int64_t bytes_per_head) {
+  const int64_t fit = kChunkBytes / std::max<int64_t>(bytes_per_head, 1);
+  const int64_t tiles = (static_cast<int64_t>(info->longest) + 127) / 128;  // the longest item
+  const int64_t steps = std::max<int64_t>(p->causal ? info->causal_steps : info->full_steps, 1);
+  const int64_t busy = (3 * 148 * tiles / 2 + steps - 1) / steps;  // 1.5 x the longest item
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(heads, std::max(fit, busy))));
+}
+
 template <typename T, int D>
 int run_packed_fwd(const sage_packed_params* p, const sage_packed_info* info, const void* plan,
                    const sage_rows* q, const sage_rows* k, const sage_rows* v, const sage_rows* o,
@@ -249,14 +294,16 @@ int run_packed_fwd(const sage_packed_params* p, const sage_packed_info* info, co
   F::Args a;
   a.group = p->Hq / p->Hkv;
   const bool heads = a.group % 2 == 0;
-  a.items = plan_list(plan, info, p->causal, !heads);
   a.o = packed_out(o);
   a.lse = lse;
   a.T = p->T;
-  a.head_groups = heads ? p->Hq / 2 : p->Hq;
+  const int ctas = heads ? p->Hq / 2 : p->Hq;  // per item
+  const int64_t kv_bytes = info->tokens * D * 2 * 2;
+  a.grid = {plan_list(plan, info, p->causal, !heads), heads ? info->tiles : info->pairs, ctas,
+            grid_chunk(p, info, ctas, kv_bytes / (heads ? a.group / 2 : a.group))};
   a.causal = p->causal;
   a.scale_log2 = packed_tau(p) * 1.4426950408889634f;
-  const int64_t grid = static_cast<int64_t>(heads ? info->tiles : info->pairs) * a.head_groups;
+  const int64_t grid = static_cast<int64_t>(a.grid.n_items) * ctas;
   return heads ? launch_packed(F::attn_fwd_kernel<T, D, true>, F::kLaunchRegs, grid, F::kThreads,
                                F::smem_bytes<T, D>(), st, tq, tk, tv, a)
                : launch_packed(F::attn_fwd_kernel<T, D, false>, F::kLaunchRegs, grid, F::kThreads,
@@ -309,7 +356,6 @@ int run_packed_bwd(const sage_packed_params* p, const sage_packed_info* info, co
   int s = launch_status();
   if (s != SAGE_OK) return s;
   B::Args a;
-  a.items = r.items;
   a.lse = lse;
   a.dvec = r.dvec;
   a.norms = r.norms;
@@ -318,14 +364,15 @@ int run_packed_bwd(const sage_packed_params* p, const sage_packed_info* info, co
   a.causal = p->causal;
   a.tau = packed_tau(p);
   a.scale_log2 = a.tau * 1.4426950408889634f;
-  a.heads = p->Hkv;
+  const int64_t pair_bytes = info->tokens * D * 2 * 2;  // two tensors of one head
+  a.grid = {r.items, info->tiles, p->Hkv, grid_chunk(p, info, p->Hkv, pair_bytes * r.group)};
   a.out[0] = packed_out(dv);
   a.out[1] = packed_out(dk);
   s = launch_packed(B::dkv_kernel<T, D>, B::kLaunchRegs,
                     static_cast<int64_t>(info->tiles) * p->Hkv, B::kThreads,
                     B::dkv_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
   if (s != SAGE_OK) return s;
-  a.heads = p->Hq;
+  a.grid = {r.items, info->tiles, p->Hq, grid_chunk(p, info, p->Hq, pair_bytes / r.group)};
   a.out[0] = packed_out(dq);
   return launch_packed(B::dq_kernel<T, D>, B::kLaunchRegs,
                        static_cast<int64_t>(info->tiles) * p->Hq, B::kThreads,
@@ -347,14 +394,9 @@ int sage_qk_norm_rope_fwd(const sage_rope_params* p, const sage_rows* q, const s
       return s;
   if (p->rotary_dim > 0 && !pos) return SAGE_ERR_INVALID_ARG;
   if (!p->norm && (gain_q || gain_k)) return SAGE_ERR_INVALID_ARG;
+  if (!aligned16(gain_q) || !aligned16(gain_k)) return SAGE_ERR_ALIGNMENT;
   sage::rope::Args a;
-  rope_args(p, &a);
-  for (int w = 0; w < 2; ++w) {
-    a.x[w] = rope_rows(w ? k : q);
-    a.y[w] = rope_rows(w ? k_out : q_out);
-    a.gain[w] = w ? gain_k : gain_q;
-  }
-  a.pos = pos;
+  rope_args(p, q, k, q_out, k_out, gain_q, gain_k, pos, &a);
   return launch_rope<false>(p, &a, nullptr, nullptr, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -377,20 +419,16 @@ int sage_qk_norm_rope_bwd(const sage_rope_params* p, const sage_rows* q, const s
   if (p->rotary_dim > 0 && !pos) return SAGE_ERR_INVALID_ARG;
   if (!p->norm && (gain_q || gain_k || dgain_q || dgain_k)) return SAGE_ERR_INVALID_ARG;
   if ((dgain_q == nullptr) != (dgain_k == nullptr)) return SAGE_ERR_INVALID_ARG;
+  if (!aligned16(gain_q) || !aligned16(gain_k)) return SAGE_ERR_ALIGNMENT;
   if (dgain_q) {
     if (!workspace || workspace_bytes < sage_qk_norm_rope_workspace_bytes(p))
       return SAGE_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SAGE_ERR_ALIGNMENT;
   }
   sage::rope::Args a;
-  rope_args(p, &a);
-  for (int w = 0; w < 2; ++w) {
-    a.x[w] = rope_rows(w ? k : q);
-    a.g[w] = rope_rows(w ? dk_out : dq_out);
-    a.y[w] = rope_rows(w ? dk : dq);
-    a.gain[w] = w ? gain_k : gain_q;
-  }
-  a.pos = pos;
+  rope_args(p, q, k, dq, dk, gain_q, gain_k, pos, &a);
+  a.g[0] = rope_rows(dq_out);
+  a.g[1] = rope_rows(dk_out);
   a.partial = dgain_q ? static_cast<float*>(workspace) : nullptr;
   return launch_rope<true>(p, &a, dgain_q, dgain_k, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -32,7 +32,7 @@ namespace bwd {
 
 constexpr int kThreads = 384;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kRowWarp = 10;
-constexpr int kLaunchRegs = 168, kComputeRegs = 232, kOtherRegs = 40;
+constexpr int kLaunchRegs = 168, kComputeRegs = 216, kOtherRegs = 72;
 static_assert(256 * kComputeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr float kLog2e = 1.4426950408889634f;
@@ -128,14 +128,21 @@ __device__ __forceinline__ float ds_factor(const uint32_t* norms) {
   return scalbnf(1.0f, e);
 }
 
+// D (+)= A B over the BT rows of tile B, A in TMEM: 32 columns at a_tmem and 32 at a_tmem + 64.
+__device__ __forceinline__ void mma_sum(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                        uint32_t idesc, bool start) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    mma_sum_half(d_tmem, a_tmem + 64 * h, b + step_mn(4 * h), idesc, start && h == 0);
+}
+
 struct Args {
-  const Item* items;
+  Grid grid;          // heads: query heads (dq_kernel), key heads (dkv_kernel)
   const float* lse;   // [Hq][T]
   const float* dvec;  // [Hq][T]
   const uint32_t* norms;
   Out out[2];         // dq_kernel: dq; dkv_kernel: dv, dk
   int64_t T;
-  int heads;          // heads of the grid: query heads (dq), key heads (dkv)
   int group;
   int causal;
   float scale_log2, tau;
@@ -157,7 +164,7 @@ __device__ __forceinline__ void probabilities(uint32_t (&x)[2][32], float c, Shi
       if (hidden(e)) z.x = -INFINITY;
       if (hidden(e + 1)) z.y = -INFINITY;
       p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-    } else if ((e & 7) == 6) {
+    } else if (poly_pair(e >> 1)) {
       p = exp2_fma2(z);
     } else {
       p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
@@ -201,16 +208,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   constexpr int NST = SM::NST;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Item it = a.items[blockIdx.x / a.heads];
-  const int kv_head = blockIdx.x % a.heads;
+  int kv_head;
+  const Item it = grid_at(a.grid, kv_head);
   const int tiles = tiles_of(it);
   // under a causal mask the list's order (most work first) is by query tile: mirrored for keys
   const int kt = a.causal ? tiles - 1 - it.tile : it.tile;
   const int first = a.causal ? kt : 0;          // first query tile that sees these keys
-  const int per_head = tiles - first;
-  const int n_all = per_head * a.group;
-  auto head_of = [&](int n) { return kv_head * a.group + n / per_head; };
-  auto tile_of = [&](int n) { return first + n % per_head; };
+  const int n_all = (tiles - first) * a.group;
+  // the steps' (query head, query tile), in order
+  struct Walk {
+    int head, tile, first, tiles;
+    __device__ __forceinline__ void next() {
+      if (++tile == tiles) {
+        tile = first;
+        ++head;
+      }
+    }
+  };
+  const Walk begin = {kv_head * a.group, first, first, tiles};
 
   if (threadIdx.x == 0) {
     sm.abort = device_aborted() ? 1 : 0;
@@ -248,23 +263,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&sm.kv_full, 2 * BT * D * 2);
         load_tile<T, D>(sm.k, &tm_k, tile_at(it, kt), kv_head, &sm.kv_full);
         load_tile<T, D>(sm.v, &tm_v, tile_at(it, kt), kv_head, &sm.kv_full);
-        for (int i = 0; i < 2 * n_all; ++i) {  // Q0 dO0 Q1 dO1 ...
-          const int st = i % NST, n = i >> 1;
-          if (i >= NST) mbar_wait(&sm.empty[st], ((i / NST) - 1) & 1, 401);
-          mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
-          load_tile<T, D>(sm.ring[st], (i & 1) ? &tm_do : &tm_q, tile_at(it, tile_of(n)),
-                          head_of(n), &sm.full[st]);
+        Ring<NST> ring;
+        Walk at = begin;
+        for (int n = 0; n < n_all; ++n, at.next()) {  // Q0 dO0 Q1 dO1 ...
+          const TileAt t = tile_at(it, at.tile);
+#pragma unroll
+          for (int w = 0; w < 2; ++w, ring.next()) {
+            const int st = ring.slot;
+            if (2 * n + w >= NST) mbar_wait(&sm.empty[st], ring.parity ^ 1, 401);
+            mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
+            load_tile<T, D>(sm.ring[st], w ? &tm_do : &tm_q, t, at.head, &sm.full[st]);
+          }
         }
       }
       __syncwarp();
     } else if (warp == kRowWarp) {
-      for (int n = 0; n < n_all; ++n) {
+      Walk at = begin;
+      for (int n = 0; n < n_all; ++n, at.next()) {
         const int b = n & 1;
         if (n >= 2) mbar_wait(&sm.vec_empty[b], ((n >> 1) - 1) & 1, 402);
-        const int64_t base = head_of(n) * a.T + it.start;
+        const int64_t base = at.head * a.T + it.start;
 #pragma unroll
         for (int r = lane; r < BT; r += 32) {
-          const int i = row_index(it, tile_of(n), r);
+          const int i = row_index(it, at.tile, r);
           sm.lse[b][r] = i >= 0 ? fmaf(a.lse[base + i], kLog2e, -Scaling<T>::kPShift) : INFINITY;
           sm.dvec[b][r] = i >= 0 ? a.dvec[base + i] : 0.0f;
         }
@@ -276,37 +297,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
         constexpr uint32_t id_g = instr_desc(1, kFmt, kFmt, false, true, BT, D);
-        const uint32_t ka = smem_u32(sm.k), va = smem_u32(sm.v);
-        auto wait_tile = [&](int i) { mbar_wait(&sm.full[i % NST], (i / NST) & 1, 411); };
-        auto product = [&](uint32_t col, uint32_t rows, int i, uint64_t* bar) {
-          wait_tile(i);
+        const uint64_t k_desc = desc_k(sm.k), v_desc = desc_k(sm.v);
+        auto product = [&](uint32_t col, uint64_t rows, const Ring<NST>& at, uint64_t* bar) {
+          mbar_wait(&sm.full[at.slot], at.parity, 411);
           tc_fence_after();
-          const uint32_t b = smem_u32(sm.ring[i % NST]);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16(tmem + col, desc_k(rows, kk), desc_k(b, kk), id_s, kk > 0 ? 1u : 0u);
+          mma_rows<D>(tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
           mma_commit(bar);
         };
-        auto accumulate = [&](uint32_t col, uint32_t from, int i, bool start) {
-          const uint32_t b = smem_u32(sm.ring[i % NST]);
-#pragma unroll
-          for (int kk = 0; kk < BT / 16; ++kk)
-            mma_f16_ts(tmem + col, tmem + from + 64 * (kk >> 2) + 8 * (kk & 3), desc_mn(b, kk),
-                       id_g, (!start || kk > 0) ? 1u : 0u);
-          mma_commit(&sm.empty[i % NST]);
-        };
+        Ring<NST> q_at, do_at;  // of Q_n and dO_n
+        do_at.next();
         mbar_wait(&sm.kv_full, 0, 410);
-        product(0, ka, 0, &sm.s_full);
-        product(kColDP, va, 1, &sm.dp_full);
+        product(0, k_desc, q_at, &sm.s_full);
+        product(kColDP, v_desc, do_at, &sm.dp_full);
         for (int n = 0; n < n_all; ++n) {
+          const bool more = n + 1 < n_all;
+          const int q_slot = q_at.slot, do_slot = do_at.slot;
+          q_at.next();
+          q_at.next();
+          do_at.next();
+          do_at.next();
           mbar_wait(&sm.p_ready, n & 1, 412);
           tc_fence_after();
-          accumulate(kColDV, 0, 2 * n + 1, n == 0);  // dV += P^T dO
-          if (n + 1 < n_all) product(0, ka, 2 * n + 2, &sm.s_full);
+          // dV += P^T dO
+          mma_sum(tmem + kColDV, tmem, desc_mn(sm.ring[do_slot]), id_g, n == 0);
+          mma_commit(&sm.empty[do_slot]);
+          if (more) product(0, k_desc, q_at, &sm.s_full);
           mbar_wait(&sm.ds_ready, n & 1, 413);
           tc_fence_after();
-          accumulate(kColDK, kColDP, 2 * n, n == 0);  // dK += dS^T Q
-          if (n + 1 < n_all) product(kColDP, va, 2 * n + 3, &sm.dp_full);
+          // dK += dS^T Q
+          mma_sum(tmem + kColDK, tmem + kColDP, desc_mn(sm.ring[q_slot]), id_g, n == 0);
+          mma_commit(&sm.empty[q_slot]);
+          if (more) product(kColDP, v_desc, do_at, &sm.dp_full);
         }
         mma_commit(&sm.done);
       }
@@ -325,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = a.scale_log2;
     float factor = 1.0f;  // dS's factor over P's
     if (Scaling<T>::kOn)
-      factor = ds_factor(a.norms + (static_cast<int64_t>(it.seq) * a.heads + kv_head) * 2);
+      factor = ds_factor(a.norms + (static_cast<int64_t>(it.seq) * a.grid.heads + kv_head) * 2);
     const float f_ds = factor * exp2f(-Scaling<T>::kPShift);
 
     auto step = [&](int n, auto masked) {
@@ -390,8 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&sm.ds_ready);
       mbar_arrive(&sm.vec_empty[b]);
     };
-    for (int n = 0; n < n_all; ++n) {
-      if (a.causal && tile_of(n) == kt)
+    Walk at = begin;
+    for (int n = 0; n < n_all; ++n, at.next()) {
+      if (a.causal && at.tile == kt)
         step(n, std::true_type{});
       else
         step(n, std::false_type{});
@@ -455,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   constexpr int NST = SM::NST;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Item it = a.items[blockIdx.x / a.heads];
-  const int head = blockIdx.x % a.heads;
+  int head;
+  const Item it = grid_at(a.grid, head);
   const int kv_head = head / a.group;
   const int tiles = tiles_of(it);
   const int n_all = a.causal ? it.tile + 1 : tiles;
@@ -494,9 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&sm.q_full, 2 * BT * D * 2);
         load_tile<T, D>(sm.q, &tm_q, tile_at(it, it.tile), head, &sm.q_full);
         load_tile<T, D>(sm.dout, &tm_do, tile_at(it, it.tile), head, &sm.q_full);
-        for (int i = 0; i < 2 * n_all; ++i) {  // K0 V0 K1 V1 ...
-          const int st = i % NST;
-          if (i >= NST) mbar_wait(&sm.empty[st], ((i / NST) - 1) & 1, 501);
+        Ring<NST> ring;
+        for (int i = 0; i < 2 * n_all; ++i, ring.next()) {  // K0 V0 K1 V1 ...
+          const int st = ring.slot;
+          if (i >= NST) mbar_wait(&sm.empty[st], ring.parity ^ 1, 501);
           mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
           load_tile<T, D>(sm.ring[st], (i & 1) ? &tm_v : &tm_k, tile_at(it, i >> 1), kv_head,
                           &sm.full[st]);
@@ -508,37 +531,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
         constexpr uint32_t id_g = instr_desc(1, kFmt, kFmt, false, true, BT, D);
-        const uint32_t qa = smem_u32(sm.q), ga = smem_u32(sm.dout);
-        auto product = [&](uint32_t col, uint32_t rows, int i, uint64_t* bar) {
-          mbar_wait(&sm.full[i % NST], (i / NST) & 1, 511);
+        const uint64_t q_desc = desc_k(sm.q), do_desc = desc_k(sm.dout);
+        auto product = [&](uint32_t col, uint64_t rows, const Ring<NST>& at, uint64_t* bar) {
+          mbar_wait(&sm.full[at.slot], at.parity, 511);
           tc_fence_after();
-          const uint32_t b = smem_u32(sm.ring[i % NST]);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16(tmem + col, desc_k(rows, kk), desc_k(b, kk), id_s, kk > 0 ? 1u : 0u);
+          mma_rows<D>(tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
           mma_commit(bar);
         };
+        Ring<NST> s_at, v_at, k_at;  // K of the next S, V of the next dP, K of the next dQ
+        v_at.next();
         mbar_wait(&sm.q_full, 0, 510);
-        product(0, qa, 0, &sm.s_full[0]);
-        product(kColQdP, ga, 1, &sm.dp_full);
-        mma_commit(&sm.empty[1 % NST]);
-        if (n_all > 1) product(128, qa, 2, &sm.s_full[1]);
+        product(0, q_desc, s_at, &sm.s_full[0]);
+        product(kColQdP, do_desc, v_at, &sm.dp_full);
+        mma_commit(&sm.empty[v_at.slot]);
+        s_at.next();
+        s_at.next();
+        v_at.next();
+        v_at.next();
+        if (n_all > 1) {
+          product(128, q_desc, s_at, &sm.s_full[1]);
+          s_at.next();
+          s_at.next();
+        }
         for (int j = 0; j < n_all; ++j) {
           if (j + 1 < n_all) {  // dP of the next key tile once this one's has been read
             mbar_wait(&sm.dp_free, j & 1, 512);
-            tc_fence_after();
-            product(kColQdP, ga, 2 * j + 3, &sm.dp_full);
-            mma_commit(&sm.empty[(2 * j + 3) % NST]);
+            product(kColQdP, do_desc, v_at, &sm.dp_full);
+            mma_commit(&sm.empty[v_at.slot]);
+            v_at.next();
+            v_at.next();
           }
           mbar_wait(&sm.ds_ready, j & 1, 513);
           tc_fence_after();
-          const uint32_t b = smem_u32(sm.ring[(2 * j) % NST]);
-#pragma unroll
-          for (int kk = 0; kk < BT / 16; ++kk)  // dQ += dS K
-            mma_f16_ts(tmem + kColQdQ, tmem + 128 * (j & 1) + 64 * (kk >> 2) + 8 * (kk & 3),
-                       desc_mn(b, kk), id_g, (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&sm.empty[(2 * j) % NST]);
-          if (j + 2 < n_all) product(128 * (j & 1), qa, 2 * j + 4, &sm.s_full[j & 1]);
+          // dQ += dS K
+          mma_sum(tmem + kColQdQ, tmem + 128 * (j & 1), desc_mn(sm.ring[k_at.slot]), id_g,
+                        j == 0);
+          mma_commit(&sm.empty[k_at.slot]);
+          k_at.next();
+          k_at.next();
+          if (j + 2 < n_all) {
+            product(128 * (j & 1), q_desc, s_at, &sm.s_full[j & 1]);
+            s_at.next();
+            s_at.next();
+          }
         }
         mma_commit(&sm.done);
       }
@@ -563,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float factor = 1.0f;
     if (Scaling<T>::kOn)
       factor = ds_factor(
-          a.norms + (static_cast<int64_t>(it.seq) * (a.heads / a.group) + kv_head) * 2);
+          a.norms + (static_cast<int64_t>(it.seq) * (a.grid.heads / a.group) + kv_head) * 2);
     const float f_ds = factor * exp2f(-Scaling<T>::kPShift);
 
     auto step = [&](int j, auto masked) {

@@ -54,6 +54,22 @@ __host__ __device__ __forceinline__ int tiles_of(const Item& it) {
   return static_cast<int>((static_cast<int64_t>(it.len) + BT - 1) / BT);
 }
 
+// The grid's order: the heads in chunks, within a chunk the items in list order (most work
+// first), within an item the chunk's heads.  A chunk is sized so that what its CTAs read over and
+// over (keys and values, or queries and gradients) stays in L2.
+struct Grid {
+  const Item* items;
+  int n_items, heads, chunk;
+};
+__device__ __forceinline__ Item grid_at(const Grid& g, int& head) {
+  const int64_t per = static_cast<int64_t>(g.n_items) * g.chunk;
+  const int c = static_cast<int>(blockIdx.x / per);
+  const int rest = static_cast<int>(blockIdx.x - c * per);
+  const int n = min(g.chunk, g.heads - c * g.chunk);
+  head = c * g.chunk + rest % n;
+  return g.items[rest / n];
+}
+
 struct Out {
   char* ptr;
   int64_t ts, hs;  // elements
@@ -84,14 +100,47 @@ __device__ __forceinline__ void load_tile(T* dst, const CUtensorMap* map, TileAt
     tma_load_4d(dst + b * BT * 64, map, b * 64, at.row, at.token, head, bar);
 }
 
-// K-major operand: rows of a tile, K = 16 channels per step kk.
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk) {
-  return smem_desc(tile + (kk >> 2) * (BT * 128) + (kk & 3) * 32, 16, 1024, kSwizzle128B);
+// Operand descriptors of a tile: the K-major form (K = 16 channels per step) and the MN-major form
+// (channels as N, 16 rows of the tile as K per step).  A step adds a constant to the address
+// field (16-byte units), so the issuing thread spends one addition per instruction.
+__device__ __forceinline__ uint64_t desc_k(const void* tile) {
+  return smem_desc(smem_u32(tile), 16, 1024, kSwizzle128B);
 }
-// MN-major operand: channels as N, 16 rows of the tile as K per step kk.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk) {
-  return smem_desc(tile + kk * 16 * 128, BT * 128, 1024, kSwizzle128B);
+__device__ __forceinline__ uint64_t desc_mn(const void* tile) {
+  return smem_desc(smem_u32(tile), BT * 128, 1024, kSwizzle128B);
 }
+__host__ __device__ constexpr uint32_t step_k(int kk) {
+  return ((kk >> 2) * (BT * 128) + (kk & 3) * 32) >> 4;
+}
+__host__ __device__ constexpr uint32_t step_mn(int kk) { return (kk * 16 * 128) >> 4; }
+
+// D = A B^T over D channels, both operands K-major tiles.
+template <int D>
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    mma_f16(d_tmem, a + step_k(kk), b + step_k(kk), idesc, kk > 0 ? 1u : 0u);
+}
+// D (+)= A B over BT / 2 rows of tile B, A in 32 TMEM columns.
+__device__ __forceinline__ void mma_sum_half(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                             uint32_t idesc, bool start) {
+#pragma unroll
+  for (int kk = 0; kk < BT / 32; ++kk)
+    mma_f16_ts(d_tmem, a_tmem + 8 * kk, b + step_mn(kk), idesc, kk > 0 || !start ? 1u : 0u);
+}
+
+// Position in a ring of N buffers, and the parity of the buffer's current round.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
 
 // 2^z for a pair as in exp2_poly2, for z <= 127 of unmasked scores: below 2^-126 the result is
 // 2^-126 instead of zero.
@@ -112,11 +161,15 @@ __device__ __forceinline__ float2 exp2_fma2(float2 z) {
                      __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
 }
 
+// Pairs whose exponentials run on the FMA pipe, the others on the special-function unit (16 a
+// clock and SM), which alone would take as long as the products.
+__device__ __forceinline__ constexpr bool poly_pair(int i) { return (i & 3) == 3; }
+
 namespace fwd {
 
 constexpr int kThreads = 384;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 232, kOtherRegs = 40;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kColO = 256;
@@ -126,7 +179,7 @@ struct Smem {
   static constexpr int NST = D == 128 ? 5 : 8;  // K / V tiles in flight
   alignas(1024) T q[2][BT * D];
   alignas(1024) T kv[NST][BT * D];
-  uint64_t q_full, full[NST], empty[NST], s_full[2], p_full[2], o_full;
+  uint64_t q_full, full[NST], empty[NST], s_full[2], p_full[2][2], o_full;
   uint32_t tmem_base;
   int abort;
 };
@@ -138,11 +191,10 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<__half, 128>() <= 232448, "shared memory exceeds the limit");
 
 struct Args {
-  const Item* items;
+  Grid grid;   // heads: CTAs per item
   Out o;
   float* lse;  // [Hq][T]
   int64_t T;
-  int head_groups;  // CTAs per item
   int group;        // query heads per key head
   int causal;
   float scale_log2;  // softmax_scale log2(e)
@@ -160,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   constexpr int NST = SM::NST;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Item it = a.items[blockIdx.x / a.head_groups];
-  const int hg = blockIdx.x % a.head_groups;
+  int hg;
+  const Item it = grid_at(a.grid, hg);
   const int head0 = HEADS ? 2 * hg : hg;
   const int kv_head = head0 / a.group;
   const bool two = HEADS || it.tile > 0;
@@ -179,7 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sm.s_full[g], 1);
-      mbar_init(&sm.p_full[g], 128);
+      mbar_init(&sm.p_full[g][0], 128);
+      mbar_init(&sm.p_full[g][1], 128);
     }
     mbar_init(&sm.o_full, 1);
     fence_barrier_init();
@@ -204,9 +257,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (two)
           load_tile<T, D>(sm.q[1], &tm_q, tile_at(it, tile_of(1)), HEADS ? head0 + 1 : head0,
                           &sm.q_full);
-        for (int i = 0; i < 2 * n0; ++i) {  // K0 V0 K1 V1 ...
-          const int st = i % NST;
-          if (i >= NST) mbar_wait(&sm.empty[st], ((i / NST) - 1) & 1, 301);
+        Ring<NST> ring;
+        for (int i = 0; i < 2 * n0; ++i, ring.next()) {  // K0 V0 K1 V1 ...
+          const int st = ring.slot;
+          if (i >= NST) mbar_wait(&sm.empty[st], ring.parity ^ 1, 301);
           mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
           load_tile<T, D>(sm.kv[st], (i & 1) ? &tm_v : &tm_k, tile_at(it, i >> 1), kv_head,
                           &sm.full[st]);
@@ -218,38 +272,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
         constexpr uint32_t id_o = instr_desc(1, kFmt, kFmt, false, true, BT, D);
-        auto scores = [&](int g, int j) {  // S_g = Q_g K_j^T
-          const uint32_t qa = smem_u32(sm.q[g]), ka = smem_u32(sm.kv[(2 * j) % NST]);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16(tmem + 128 * g, desc_k(qa, kk), desc_k(ka, kk), id_s, kk > 0 ? 1u : 0u);
+        const uint64_t q_desc[2] = {desc_k(sm.q[0]), desc_k(sm.q[1])};
+        auto scores = [&](int g, uint64_t k_desc) {  // S_g = Q_g K^T
+          mma_rows<D>(tmem + 128 * g, q_desc[g], k_desc, id_s);
           mma_commit(&sm.s_full[g]);
         };
-        auto wait_tile = [&](int i) { mbar_wait(&sm.full[i % NST], (i / NST) & 1, 311); };
+        Ring<NST> v_at, k_at;  // of V_j and K_(j + 1)
         mbar_wait(&sm.q_full, 0, 310);
-        wait_tile(0);
+        mbar_wait(&sm.full[0], 0, 311);
         tc_fence_after();
-        scores(0, 0);
-        if (n1 > 0) scores(1, 0);
+        scores(0, desc_k(sm.kv[0]));
+        if (n1 > 0) scores(1, desc_k(sm.kv[0]));
         mma_commit(&sm.empty[0]);
+        v_at.next();
+        k_at = v_at;
+        k_at.next();
         for (int j = 0; j < n0; ++j) {
-          wait_tile(2 * j + 1);
-          if (j + 1 < n0) wait_tile(2 * j + 2);
-          const uint32_t va = smem_u32(sm.kv[(2 * j + 1) % NST]);
+          const bool more = j + 1 < n0;
+          mbar_wait(&sm.full[v_at.slot], v_at.parity, 311);
+          if (more) mbar_wait(&sm.full[k_at.slot], k_at.parity, 311);
+          const uint64_t v_desc = desc_mn(sm.kv[v_at.slot]);
+          const uint64_t k_desc = desc_k(sm.kv[k_at.slot]);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const int n = g == 0 ? n0 : n1;
             if (j >= n) continue;
-            mbar_wait(&sm.p_full[g], j & 1, 312);
-            tc_fence_after();
+            // in halves of the keys, so that the first runs during the second's exponentials
 #pragma unroll
-            for (int kk = 0; kk < BT / 16; ++kk)
-              mma_f16_ts(tmem + kColO + 128 * g, tmem + 128 * g + 8 * kk, desc_mn(va, kk), id_o,
-                         (j > 0 || kk > 0) ? 1u : 0u);
-            if (j + 1 < n) scores(g, j + 1);
+            for (int h = 0; h < 2; ++h) {
+              mbar_wait(&sm.p_full[g][h], j & 1, 312);
+              tc_fence_after();
+              mma_sum_half(tmem + kColO + 128 * g, tmem + 128 * g + 32 * h, v_desc + step_mn(4 * h),
+                           id_o, j == 0 && h == 0);
+            }
+            if (j + 1 < n) scores(g, k_desc);
           }
-          mma_commit(&sm.empty[(2 * j + 1) % NST]);
-          if (j + 1 < n0) mma_commit(&sm.empty[(2 * j + 2) % NST]);
+          mma_commit(&sm.empty[v_at.slot]);
+          if (more) mma_commit(&sm.empty[k_at.slot]);
+          v_at.next();
+          v_at.next();
+          k_at.next();
+          k_at.next();
         }
         mma_commit(&sm.o_full);
       }
@@ -333,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 z = __ffma2_rn(
               make_float2(__uint_as_float(x[q][ee]), __uint_as_float(x[q][ee + 1])), c2, n2);
           float2 p;
-          if (!MASK && (e & 7) == 6)
+          if (!MASK && poly_pair(e >> 1))
             p = exp2_fma2(z);
           else
             p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
@@ -344,10 +407,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[e >> 1] = Cvt<T>::pack2(p.x, p.y);
         }
         tmem_st32(s_at + 32 * hh, w);
+        tmem_st_wait();  // of O too, where it was rescaled
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[g][hh]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&sm.p_full[g]);
       l += (sum.x + sum.y) + (sum2.x + sum2.y);
     };
     const bool ragged = tiles_of(it) * BT != it.len;

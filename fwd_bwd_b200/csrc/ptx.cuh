@@ -132,6 +132,17 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// 4-D tiled store of a shared-memory box (coordinates not negative; elements past the map's end
+// are not written).  Tracked by bulk groups.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int c0,
+                                             int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::
+          "l"(reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(src))
+      : "memory");
+}
+
 // Contiguous global -> shared copy of `bytes` (a multiple of 16; both addresses 16-byte
 // aligned), completing `bar`'s transaction count.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,

@@ -4,21 +4,25 @@
 //   forward:   xhat = x inv, inv = 1 / sqrt(mean x^2 + eps); y = R (xhat gain)
 //   backward:  g = R^T dy; dgain += g xhat; gx = g gain; dx = inv (gx - xhat mean(gx xhat))
 //
-// Bound: HBM (about 10 flops per byte-pair moved; the forward moves 4 bytes per element, the
-// backward 6).  Layout: a row of d channels is held by d/8 lanes (one 16-byte load each), and
-// such a group of lanes walks the heads of one token, because the rotation's angles depend on
-// the token only: its 8 sines and cosines per lane are computed once per token and used for
-// every head of the group's chunk.
+// Bound: HBM (the forward moves 4 bytes per element, the backward 6).  Layout: a row of d
+// channels is held by d/8 lanes, each with two groups of 4 channels (two 8-byte loads): the two
+// halves of the same 4 pairs, so the rotation needs no exchange between lanes and a lane needs
+// 4 sines and cosines.  Such a group of lanes walks the heads of one token, q's and then k's,
+// because the angles depend on the token only, a few rows at a time so that their loads and their
+// row sums overlap.
 //
 // Angles: frequency i as F_i = inv_freq_i / (2 pi) * 2^64 modulo 2^64, so position * F_i
 // modulo 2^64 is the angle's fraction of a turn, with all full turns dropped exactly: the same
-// accuracy at position 2^31 as at 1.  Its top 32 bits, read as a signed fraction of a half turn,
-// go to sincospif in float32 (angle error below 2^-23).
+// accuracy at position 2^31 as at 1.  Its top 32 bits, a signed fraction of a half turn, become
+// an angle in [-pi, pi], where the fast sine and cosine are within 2^-21 of the true ones (they
+// multiply values that are rounded to 2^-9 or 2^-11 afterwards).
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "rowops.cuh"
@@ -44,203 +48,296 @@ struct Args {
   int64_t pos_as, pos_bs;
   uint64_t freq[64];
   int bound[kMaxAxes - 1];  // first pair of axes 1, 2, 3
-  int tokens, N, Hq, Hkv;
-  int chunks, per_chunk;  // the heads of a token are cut into `chunks` of per_chunk
-  int rotary, interleaved, n_axes, pos64, norm;
+  int tokens, N, Hq, H;     // H: heads of q and k
+  int chunks, per_chunk;    // the heads of a token are cut into `chunks` of per_chunk
+  int rotary, pos64, norm;
   float eps;
 };
 
-// Angle data of one lane: the cosine and (signed) sine of its 8 channels' pairs.
-template <int D>
-struct Turn {
-  float c[8], s[8];
-  bool rot;  // the lane's channels are rotated
-
-  // y = R v (SIGN = 1) or R^T v (SIGN = -1) of the lane's 8 channels.  partner: lane that
-  // holds the other channels of the pairs (half-split), or this lane itself.
-  template <int SIGN>
-  __device__ __forceinline__ void apply(float (&v)[8], bool interleaved, int partner,
-                                        uint32_t mask) const {
-    if (interleaved) {
-      if (!rot) return;
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float a = v[e], b = v[e + 1];
-        v[e] = fmaf(a, c[e], SIGN * b * s[e]);
-        v[e + 1] = fmaf(b, c[e], SIGN * a * s[e + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_sync(mask, v[e], partner);
-        if (rot) v[e] = fmaf(v[e], c[e], SIGN * o * s[e]);
-      }
-    }
-  }
+// The 8 channels of a lane as 4 pairs (a, b), two pairs per packed operation.
+struct Pairs {
+  float2 a[2], b[2];
 };
 
-template <typename T, int D, bool BWD>
-__global__ void __launch_bounds__(kThreads, BWD ? 2 : 4)
-    qk_rope_kernel(const __grid_constant__ Args a) {
-  constexpr int LPR = D / 8;             // lanes per row
-  constexpr int GROUPS = kThreads / LPR; // groups of lanes per block
-  __shared__ uint64_t freq[64];
-  __shared__ float red[BWD ? GROUPS : 1][BWD ? D : 1];
-  for (int i = threadIdx.x; i < 64; i += kThreads) freq[i] = a.freq[i];
-  __syncthreads();
-
-  const int lane = threadIdx.x & 31;
-  const int l = lane % LPR;          // lane within the row
-  const int base = lane - l;         // first lane of the row
-  const uint32_t mask = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << base;
-  const int half = a.rotary >> 1;
-  const int c0 = 8 * l;              // first channel of the lane
-  const bool rot = c0 < a.rotary;
-  int partner = lane, pair0 = 0;
-  float sign = 1.0f;
-  if (a.interleaved) {
-    pair0 = c0 >> 1;
-  } else if (rot) {
-    const bool upper = c0 >= half;
-    partner = upper ? lane - half / 8 : lane + half / 8;
-    pair0 = upper ? c0 - half : c0;
-    sign = upper ? 1.0f : -1.0f;  // y_lo = lo c - hi s, y_hi = hi c + lo s
+// u: the lane's first 4 channels, v: its second 4.  INTER: pairs are neighbouring channels;
+// otherwise channel e of u with channel e of v.
+template <typename T, bool INTER>
+__device__ __forceinline__ Pairs unpack(const uint2& u, const uint2& v) {
+  float f[8];
+  Cvt<T>::load8(make_uint4(u.x, u.y, v.x, v.y), f);
+  Pairs p;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    p.a[i] = INTER ? make_float2(f[4 * i], f[4 * i + 2]) : make_float2(f[2 * i], f[2 * i + 1]);
+    p.b[i] = INTER ? make_float2(f[4 * i + 1], f[4 * i + 3])
+                   : make_float2(f[4 + 2 * i], f[5 + 2 * i]);
   }
-  float gain[2][8];
+  return p;
+}
+template <typename T, bool INTER>
+__device__ __forceinline__ void pack(const Pairs& p, uint2& u, uint2& v) {
+  if (INTER) {
+    u = make_uint2(Cvt<T>::pack2(p.a[0].x, p.b[0].x), Cvt<T>::pack2(p.a[0].y, p.b[0].y));
+    v = make_uint2(Cvt<T>::pack2(p.a[1].x, p.b[1].x), Cvt<T>::pack2(p.a[1].y, p.b[1].y));
+  } else {
+    u = make_uint2(Cvt<T>::pack2(p.a[0].x, p.a[0].y), Cvt<T>::pack2(p.a[1].x, p.a[1].y));
+    v = make_uint2(Cvt<T>::pack2(p.b[0].x, p.b[0].y), Cvt<T>::pack2(p.b[1].x, p.b[1].y));
+  }
+}
+
+template <typename T, int D, bool INTER, bool BWD>
+__global__ void __launch_bounds__(kThreads, BWD ? 2 : 3)
+    qk_rope_kernel(const __grid_constant__ Args a) {
+  constexpr int LPR = D / 8;              // lanes per row
+  constexpr int GROUPS = kThreads / LPR;  // groups of lanes per block
+  constexpr int UN = BWD ? 2 : 4;  // rows at a time
+  const int lane = threadIdx.x & 31;
+  const int l = lane % LPR;               // lane within the row
+  const uint32_t mask = ((1u << LPR) - 1u) << (lane - l);
+  const int half = a.rotary >> 1;
+  // first channels of the lane's two groups
+  const bool rot = INTER ? 8 * l < a.rotary : 4 * l < half;
+  int cu, cv;
+  if (INTER) {
+    cu = 8 * l;
+    cv = cu + 4;
+  } else if (rot) {
+    cu = 4 * l;
+    cv = cu + half;
+  } else {
+    cu = a.rotary + 8 * (l - half / 4);
+    cv = cu + 4;
+  }
+  const int dv = cv - cu;
+  Pairs dgain[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) gain[w][e] = a.gain[w] ? a.gain[w][c0 + e] : 1.0f;
-  float dgain[2][8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) dgain[0][e] = dgain[1][e] = 0.0f;
+    for (int i = 0; i < 2; ++i) dgain[w].a[i] = dgain[w].b[i] = make_float2(0.0f, 0.0f);
 
-  const int64_t units = static_cast<int64_t>(a.tokens) * a.chunks;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS;
-  const int H = a.Hq + a.Hkv;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * GROUPS + threadIdx.x / LPR; u < units;
-       u += step) {
-    const int token = static_cast<int>(u / a.chunks);
-    const int chunk = static_cast<int>(u - static_cast<int64_t>(token) * a.chunks);
-    const int b = token / a.N, n = token - b * a.N;
-    Turn<D> t;
-    t.rot = rot;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      t.c[e] = 1.0f;
-      t.s[e] = 0.0f;
-    }
+  // a block's unit: GROUPS tokens, one chunk of their heads (all lanes of a warp then work on the
+  // same tensor); neighbouring blocks take the same tokens' chunks
+  const int tiles = (a.tokens + GROUPS - 1) / GROUPS;
+  const int64_t units = static_cast<int64_t>(tiles) * a.chunks;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int tile = static_cast<int>(unit / a.chunks);
+    const int lo = static_cast<int>(unit - static_cast<int64_t>(tile) * a.chunks) * a.per_chunk;
+    const int hi = min(a.H, lo + a.per_chunk);
+    const int token = tile * GROUPS + threadIdx.x / LPR;
+    if (token >= a.tokens) continue;
+    const int b = token < a.N ? 0 : token / a.N, n = token - b * a.N;
+    auto row_at = [&](const Rows (&r)[2], int h) {
+      const int w = h < a.Hq ? 0 : 1;
+      return reinterpret_cast<T*>(r[w].ptr) + b * r[w].bs + static_cast<int64_t>(n) * r[w].ts +
+             static_cast<int64_t>(h - (w ? a.Hq : 0)) * r[w].hs + cu;
+    };
+    int64_t at[4];  // the positions of the lane's pairs
     if (rot) {
-      uint64_t p[kMaxAxes];
 #pragma unroll
-      for (int ax = 0; ax < kMaxAxes; ++ax) {
-        if (ax >= a.n_axes) {
-          p[ax] = 0;
-          continue;
-        }
-        const int64_t at = ax * a.pos_as + b * a.pos_bs + n;
-        p[ax] = a.pos64 ? static_cast<uint64_t>(static_cast<const int64_t*>(a.pos)[at])
-                        : static_cast<uint64_t>(
-                              static_cast<int64_t>(static_cast<const int32_t*>(a.pos)[at]));
-      }
-      auto angle = [&](int i, float& s, float& c) {
-        uint64_t pp = p[0];
-        if (i >= a.bound[0]) pp = p[1];
-        if (i >= a.bound[1]) pp = p[2];
-        if (i >= a.bound[2]) pp = p[3];
-        const int32_t top = static_cast<int32_t>((pp * freq[i]) >> 32);
-        sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-      };
-      if (a.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          float s, c;
-          angle(pair0 + (e >> 1), s, c);
-          t.c[e] = t.c[e + 1] = c;
-          t.s[e] = -s;
-          t.s[e + 1] = s;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float s, c;
-          angle(pair0 + e, s, c);
-          t.c[e] = c;
-          t.s[e] = sign * s;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int i = 4 * l + e;
+        const int axis = (i >= a.bound[0]) + (i >= a.bound[1]) + (i >= a.bound[2]);
+        const int64_t from = axis * a.pos_as + b * a.pos_bs + n;
+        at[e] = a.pos64 ? __ldg(static_cast<const long long*>(a.pos) + from)
+                        : __ldg(static_cast<const int32_t*>(a.pos) + from);
       }
     }
-    const int h_end = min(H, (chunk + 1) * a.per_chunk);
-    // one tensor after the other: a chunk may hold heads of both
+    float2 cs[2], sn[2], ns[2];
+    bool fresh = rot;  // the angles are still to be computed: after the first rows' loads
+    auto angles = [&]() {
+      float s[4], c[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int32_t top =
+            static_cast<int32_t>((static_cast<uint64_t>(at[e]) * a.freq[4 * l + e]) >> 32);
+        __sincosf(static_cast<float>(top) * 1.4629180792671596e-9f, &s[e], &c[e]);  // pi 2^-31
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        cs[i] = make_float2(c[2 * i], c[2 * i + 1]);
+        sn[i] = make_float2(s[2 * i], s[2 * i + 1]);
+        ns[i] = make_float2(-sn[i].x, -sn[i].y);
+      }
+      fresh = false;
+    };
+    int h = lo;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const int first = w == 0 ? 0 : a.Hq;
-      const int lo = max(chunk * a.per_chunk, first) - first;
-      const int hi = min(h_end, w == 0 ? a.Hq : H) - first;
-      const T* xp = reinterpret_cast<const T*>(a.x[w].ptr) + b * a.x[w].bs +
-                    static_cast<int64_t>(n) * a.x[w].ts + c0;
-      const T* gp = BWD ? reinterpret_cast<const T*>(a.g[w].ptr) + b * a.g[w].bs +
-                              static_cast<int64_t>(n) * a.g[w].ts + c0
-                        : nullptr;
-      T* yp = reinterpret_cast<T*>(a.y[w].ptr) + b * a.y[w].bs +
-              static_cast<int64_t>(n) * a.y[w].ts + c0;
-      constexpr int UN = BWD ? 2 : 4;  // rows in flight per group
-      for (int h0 = lo; h0 < hi; h0 += UN) {
-        uint4 xr[UN], gr[UN];
+      const int end = w == 0 ? min(hi, a.Hq) : hi;
+      if (h >= end) continue;
+      const T* xp = row_at(a.x, h);
+      const T* gp = BWD ? row_at(a.g, h) : nullptr;
+      T* yp = row_at(a.y, h);
+      const int64_t xs = a.x[w].hs, gs = a.g[w].hs, ys = a.y[w].hs;
+      Pairs gain;
 #pragma unroll
-        for (int i = 0; i < UN; ++i) {
-          const int h = min(h0 + i, hi - 1);
-          xr[i] = __ldcs(reinterpret_cast<const uint4*>(xp + h * a.x[w].hs));
-          if (BWD) gr[i] = __ldcs(reinterpret_cast<const uint4*>(gp + h * a.g[w].hs));
-        }
-#pragma unroll
-        for (int i = 0; i < UN; ++i) {
-          if (h0 + i >= hi) break;
-          float x[8];
-          Cvt<T>::load8(xr[i], x);
-          float inv = 1.0f;
-          if (a.norm) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-            inv = 1.0f / sqrtf(row_sum<LPR>(ss, mask) * (1.0f / D) + a.eps);
-          }
-          if (!BWD) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= inv * gain[w][e];
-            t.template apply<1>(x, a.interleaved, partner, mask);
-            *reinterpret_cast<uint4*>(yp + (h0 + i) * a.y[w].hs) = pack8<T>(x);
-          } else {
-            float g[8];
-            Cvt<T>::load8(gr[i], g);
-            t.template apply<-1>(g, a.interleaved, partner, mask);
-            if (a.norm) {
-              float dot = 0.0f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                x[e] *= inv;
-                dgain[w][e] = fmaf(g[e], x[e], dgain[w][e]);
-                g[e] *= gain[w][e];
-                dot = fmaf(g[e], x[e], dot);
-              }
-              dot = row_sum<LPR>(dot, mask) * (1.0f / D);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) g[e] = inv * fmaf(-x[e], dot, g[e]);
-            }
-            *reinterpret_cast<uint4*>(yp + (h0 + i) * a.y[w].hs) = pack8<T>(g);
-          }
+      for (int i = 0; i < 2; ++i) gain.a[i] = gain.b[i] = make_float2(1.0f, 1.0f);
+      if (a.gain[w]) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(a.gain[w] + cu));
+        const float4 v = __ldg(reinterpret_cast<const float4*>(a.gain[w] + cv));
+        if (INTER) {
+          gain.a[0] = make_float2(u.x, u.z);
+          gain.b[0] = make_float2(u.y, u.w);
+          gain.a[1] = make_float2(v.x, v.z);
+          gain.b[1] = make_float2(v.y, v.w);
+        } else {
+          gain.a[0] = make_float2(u.x, u.y);
+          gain.a[1] = make_float2(u.z, u.w);
+          gain.b[0] = make_float2(v.x, v.y);
+          gain.b[1] = make_float2(v.z, v.w);
         }
       }
+      // R rows from h on
+      auto rows = [&](auto count) {
+        constexpr int R = decltype(count)::value;
+        uint2 xu[R], xv[R], gu[R], gv[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          xu[i] = __ldcs(reinterpret_cast<const uint2*>(xp));
+          xv[i] = __ldcs(reinterpret_cast<const uint2*>(xp + dv));
+          xp += xs;
+          if (BWD) {
+            gu[i] = __ldcs(reinterpret_cast<const uint2*>(gp));
+            gv[i] = __ldcs(reinterpret_cast<const uint2*>(gp + dv));
+            gp += gs;
+          }
+        }
+        if (fresh) angles();
+        if (!BWD) {
+          float inv[R];
+          if (a.norm) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              const Pairs x = unpack<T, INTER>(xu[i], xv[i]);
+              float2 ss = __fmul2_rn(x.a[0], x.a[0]);
+              ss = __ffma2_rn(x.b[0], x.b[0], ss);
+              ss = __ffma2_rn(x.a[1], x.a[1], ss);
+              ss = __ffma2_rn(x.b[1], x.b[1], ss);
+              inv[i] = ss.x + ss.y;
+            }
+#pragma unroll
+            for (int o = LPR / 2; o >= 1; o >>= 1)
+#pragma unroll
+              for (int i = 0; i < R; ++i) inv[i] += __shfl_xor_sync(mask, inv[i], o);
+#pragma unroll
+            for (int i = 0; i < R; ++i) inv[i] = rsqrtf(fmaf(inv[i], 1.0f / D, a.eps));
+          }
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            Pairs x = unpack<T, INTER>(xu[i], xv[i]);
+            if (a.norm) {
+              const float2 inv2 = make_float2(inv[i], inv[i]);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                x.a[k] = __fmul2_rn(__fmul2_rn(x.a[k], inv2), gain.a[k]);
+                x.b[k] = __fmul2_rn(__fmul2_rn(x.b[k], inv2), gain.b[k]);
+              }
+            }
+            if (rot) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float2 p = x.a[k], q = x.b[k];
+                x.a[k] = __ffma2_rn(p, cs[k], __fmul2_rn(q, ns[k]));
+                x.b[k] = __ffma2_rn(q, cs[k], __fmul2_rn(p, sn[k]));
+              }
+            }
+            uint2 u, v;
+            pack<T, INTER>(x, u, v);
+            *reinterpret_cast<uint2*>(yp) = u;
+            *reinterpret_cast<uint2*>(yp + dv) = v;
+            yp += ys;
+          }
+        } else {
+          Pairs g[R];
+          float2 sums[R];  // of x^2 and of gx x: xhat = x inv, inv known only after them
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            g[i] = unpack<T, INTER>(gu[i], gv[i]);
+            if (rot) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float2 p = g[i].a[k], q = g[i].b[k];
+                g[i].a[k] = __ffma2_rn(p, cs[k], __fmul2_rn(q, sn[k]));
+                g[i].b[k] = __ffma2_rn(q, cs[k], __fmul2_rn(p, ns[k]));
+              }
+            }
+            if (a.norm) {
+              const Pairs x = unpack<T, INTER>(xu[i], xv[i]);
+              float2 ss = make_float2(0.0f, 0.0f), dot = ss;
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                ss = __ffma2_rn(x.a[k], x.a[k], __ffma2_rn(x.b[k], x.b[k], ss));
+                dot = __ffma2_rn(__fmul2_rn(g[i].a[k], gain.a[k]), x.a[k], dot);
+                dot = __ffma2_rn(__fmul2_rn(g[i].b[k], gain.b[k]), x.b[k], dot);
+              }
+              sums[i] = make_float2(ss.x + ss.y, dot.x + dot.y);
+            }
+          }
+          if (a.norm) {
+#pragma unroll
+            for (int o = LPR / 2; o >= 1; o >>= 1)
+#pragma unroll
+              for (int i = 0; i < R; ++i)
+                sums[i] = __fadd2_rn(sums[i], make_float2(__shfl_xor_sync(mask, sums[i].x, o),
+                                                          __shfl_xor_sync(mask, sums[i].y, o)));
+          }
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            if (a.norm) {
+              Pairs x = unpack<T, INTER>(xu[i], xv[i]);
+              const float inv = rsqrtf(fmaf(sums[i].x, 1.0f / D, a.eps));
+              // xhat mean(gx xhat) = xhat * (mean(gx x) inv)
+              const float mean = sums[i].y * (1.0f / D) * inv;
+              const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-mean, -mean);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                x.a[k] = __fmul2_rn(x.a[k], inv2);
+                x.b[k] = __fmul2_rn(x.b[k], inv2);
+                dgain[w].a[k] = __ffma2_rn(g[i].a[k], x.a[k], dgain[w].a[k]);
+                dgain[w].b[k] = __ffma2_rn(g[i].b[k], x.b[k], dgain[w].b[k]);
+                g[i].a[k] = __fmul2_rn(
+                    __ffma2_rn(x.a[k], neg2, __fmul2_rn(g[i].a[k], gain.a[k])), inv2);
+                g[i].b[k] = __fmul2_rn(
+                    __ffma2_rn(x.b[k], neg2, __fmul2_rn(g[i].b[k], gain.b[k])), inv2);
+              }
+            }
+            uint2 u, v;
+            pack<T, INTER>(g[i], u, v);
+            *reinterpret_cast<uint2*>(yp) = u;
+            *reinterpret_cast<uint2*>(yp + dv) = v;
+            yp += ys;
+          }
+        }
+        h += R;
+      };
+      while (h + UN <= end) rows(std::integral_constant<int, UN>{});
+      while (h < end) rows(std::integral_constant<int, 1>{});
     }
   }
   if constexpr (BWD) {
     if (a.partial == nullptr) return;
     // the block's sums, groups in order
+    __shared__ float red[GROUPS][D];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       __syncthreads();
+      float* row = red[threadIdx.x / LPR];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) red[threadIdx.x / LPR][c0 + e] = dgain[w][e];
+      for (int i = 0; i < 2; ++i) {
+        const float2 p = dgain[w].a[i], q = dgain[w].b[i];
+        if (INTER) {
+          float* at = row + (i == 0 ? cu : cv);
+          at[0] = p.x;
+          at[1] = q.x;
+          at[2] = p.y;
+          at[3] = q.y;
+        } else {
+          row[cu + 2 * i] = p.x;
+          row[cu + 2 * i + 1] = p.y;
+          row[cv + 2 * i] = q.x;
+          row[cv + 2 * i + 1] = q.y;
+        }
+      }
       __syncthreads();
       for (int c = threadIdx.x; c < D; c += kThreads) {
         float sum = 0.0f;

@@ -14,8 +14,7 @@ import torch
 
 from ._lib import SageError, SagePackedInfo, SagePackedParams, check, lib
 from ._lib import SAGE_ERR_INVALID_ARG
-from .ops import _DTYPES, _stream
-from .rope import _check_rows, _rows, _supported
+from .rope import _call, _like, _rows, _supported, _type_and_device
 
 
 class Batch:
@@ -46,6 +45,7 @@ class Batch:
         check("sage_packed_plan_fill", lib().sage_packed_plan_fill(
             arr, len(self.lengths), host.data_ptr(), n, ctypes.byref(self.info)))
         self.plan = host.to(torch.device(device))
+        self.plan_ptr = self.plan.data_ptr()
         self.tokens = int(self.info.tokens)
 
     @property
@@ -58,38 +58,39 @@ class Batch:
 
 
 def _params(q, k, v, batch: Batch, causal: bool, softmax_scale: float) -> SagePackedParams:
-    for name, x in (("q", q), ("k", k), ("v", v)):
-        if x.dim() != 3:
-            raise ValueError(f"{name} must be [T, H, d]")
-        _check_rows(name, x)
-    if k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [T, H, d]")
+    dtype, dev = _type_and_device(q)
+    (T, Hq, d), (Tk, Hkv, dk) = q.shape, k.shape
+    if k.shape != v.shape or Tk != T or dk != d:
         raise ValueError("q, k and v must hold the same tokens and channels, k and v the same heads")
-    if not (q.dtype == k.dtype == v.dtype and q.device == k.device == v.device == batch.device):
-        raise ValueError("q, k, v and the batch must have one type and device")
-    T, Hq, d = q.shape
-    if k.shape[1] == 0 or Hq % k.shape[1]:
+    if (q.dtype != k.dtype or q.dtype != v.dtype or k.get_device() != dev
+            or v.get_device() != dev):
+        raise ValueError("q, k and v must have one type and device")
+    if Hkv == 0 or Hq % Hkv:
         raise ValueError("the query heads must be a multiple of the key heads")
     if T < batch.tokens:
         raise ValueError(f"the batch holds {batch.tokens} tokens, the tensors {T} rows")
-    return SagePackedParams(T, Hq, k.shape[1], d, _DTYPES[q.dtype], int(causal),
-                            float(softmax_scale))
+    return SagePackedParams(T, Hq, Hkv, d, dtype, bool(causal), softmax_scale)
 
 
-def _out(name: str, x: Optional[torch.Tensor], like: torch.Tensor, batch: Batch) -> torch.Tensor:
-    """The caller's output, or a new one whose rows behind the last sequence are zero."""
-    if x is None:
-        x = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-        if like.shape[0] > batch.tokens:
-            x[batch.tokens:].zero_()
-        return x
-    _check_rows(name, x, like)
+def _new(like: torch.Tensor, batch: Batch) -> torch.Tensor:
+    """An output for ``like``'s shape whose rows behind the last sequence are zero."""
+    x = like.new_empty(like.shape)
+    if like.shape[0] > batch.tokens:
+        x[batch.tokens:].zero_()
     return x
 
 
 def _check_lse(lse: torch.Tensor, q: torch.Tensor) -> None:
     if (lse.dtype != torch.float32 or lse.shape != (q.shape[1], q.shape[0])
-            or lse.device != q.device or not lse.is_contiguous()):
+            or lse.get_device() != q.get_device() or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [Hq, T] tensor on q's device")
+
+
+def _check_batch(q: torch.Tensor, batch: Batch) -> None:
+    if batch.plan.get_device() != q.get_device():
+        raise ValueError("the batch must be on q's device")
 
 
 def attn_fwd(q, k, v, batch: Batch, causal: bool = True, softmax_scale: float = 0.0, o=None,
@@ -102,18 +103,18 @@ def attn_fwd(q, k, v, batch: Batch, causal: bool = True, softmax_scale: float = 
     when the caller gives them, zero otherwise.  Given outputs must not overlap the inputs.
     """
     prm = _params(q, k, v, batch, causal, softmax_scale)
-    o = _out("o", o, q, batch)
+    _check_batch(q, batch)
+    o = _new(q, batch) if o is None else o
     if lse is None:
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-        if q.shape[0] > batch.tokens:
+        lse = q.new_empty((prm.Hq, prm.T), dtype=torch.float32)
+        if prm.T > batch.tokens:
             lse[:, batch.tokens:].zero_()
-    _check_lse(lse, q)
-    if batch.tokens == 0:
-        return o, lse
-    with torch.cuda.device(q.device):
-        check("sage_packed_attn_fwd", lib().sage_packed_attn_fwd(
-            ctypes.byref(prm), ctypes.byref(batch.info), batch.plan.data_ptr(), _rows(q),
-            _rows(k), _rows(v), _rows(o), lse.data_ptr(), _stream(q.device)))
+    else:
+        _check_lse(lse, q)
+    rows_o = _like("o", o, q)
+    if batch.tokens:
+        _call("sage_packed_attn_fwd", q.get_device(), prm, batch.info, batch.plan_ptr, _rows(q),
+              _rows(k), _rows(v), rows_o, lse.data_ptr())
     return o, lse
 
 
@@ -125,29 +126,28 @@ def attn_bwd(q, k, v, o, lse, dout, batch: Batch, causal: bool = True, softmax_s
     ``workspace_bytes`` elements; calls that share one must be ordered.
     """
     prm = _params(q, k, v, batch, causal, softmax_scale)
-    _check_rows("o", o, q)
-    _check_rows("dout", dout, q)
+    rows = (_rows(q), _rows(k), _rows(v), _like("o", o, q))
+    rows_do = _like("dout", dout, q)
+    _check_batch(q, batch)
     _check_lse(lse, q)
-    dq, dk, dv = (_out(n, x, like, batch)
-                  for n, x, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)))
+    dq = _new(q, batch) if dq is None else dq
+    dk = _new(k, batch) if dk is None else dk
+    dv = _new(v, batch) if dv is None else dv
+    grads = (_like("dq", dq, q), _like("dk", dk, k), _like("dv", dv, k))
     if batch.tokens == 0:
         return dq, dk, dv
     if workspace is None:
         workspace = torch.empty(_workspace_bytes(prm, batch), dtype=torch.uint8, device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
+    elif workspace.get_device() != q.get_device() or not workspace.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on q's device")
-    with torch.cuda.device(q.device):
-        check("sage_packed_attn_bwd", lib().sage_packed_attn_bwd(
-            ctypes.byref(prm), ctypes.byref(batch.info), batch.plan.data_ptr(), _rows(q),
-            _rows(k), _rows(v), _rows(o), lse.data_ptr(), _rows(dout), _rows(dq), _rows(dk),
-            _rows(dv), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _stream(q.device)))
+    _call("sage_packed_attn_bwd", q.get_device(), prm, batch.info, batch.plan_ptr, *rows,
+          lse.data_ptr(), rows_do, *grads, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return dq, dk, dv
 
 
 def _workspace_bytes(prm: SagePackedParams, batch: Batch) -> int:
-    return int(lib().sage_packed_attn_bwd_workspace_bytes(ctypes.byref(prm),
-                                                          ctypes.byref(batch.info)))
+    return int(lib().sage_packed_attn_bwd_workspace_bytes(prm, batch.info))
 
 
 def workspace_bytes(q, k, v, batch: Batch) -> int:

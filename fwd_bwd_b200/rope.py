@@ -14,7 +14,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from ._lib import SageRopeParams, SageRows, check, lib
-from .ops import _DTYPES, _stream
+from .ops import _DTYPES
 
 
 class Rope:
@@ -54,26 +54,12 @@ class Rope:
         if not (math.isfinite(self.eps) and self.eps >= 0):
             raise ValueError("eps must be finite and not negative")
         self._freq = (ctypes.c_double * max(half, 1))(*self.inv_freq)
+        self._freq_ptr = ctypes.addressof(self._freq)
         self._sections = (ctypes.c_int * 4)(*(self.sections if half else []))
 
     @property
     def axes(self) -> int:
         return len(self.sections) if self.rotary_dim else 0
-
-
-def _shape(x: torch.Tensor) -> Tuple[int, int, int, int]:
-    """(B, N, H, d) of packed [T, H, d] or batched [B, H, N, d] vectors."""
-    if x.dim() == 3:
-        return (1, x.shape[0], x.shape[1], x.shape[2])
-    if x.dim() == 4:
-        return (x.shape[0], x.shape[2], x.shape[1], x.shape[3])
-    raise ValueError("q and k must be [T, H, d] or [B, H, N, d]")
-
-
-def _strides(x: torch.Tensor) -> Tuple[int, int, int]:
-    """Batch, token and head strides (elements)."""
-    s = x.stride()
-    return (0, s[0], s[1]) if x.dim() == 3 else (s[0], s[2], s[1])
 
 
 def _supported(x: torch.Tensor) -> bool:
@@ -87,61 +73,75 @@ def _supported(x: torch.Tensor) -> bool:
 
 
 def _rows(x: torch.Tensor) -> SageRows:
-    return SageRows(x.data_ptr(), *_strides(x))
+    """The tensor's description for the C ABI, which checks pointers, alignment, the other strides
+    and overlap within an output."""
+    s = x.stride()
+    if s[-1] != 1:
+        raise ValueError("channels must be contiguous")
+    if len(s) == 3:
+        return SageRows(x.data_ptr(), 0, s[0], s[1])
+    return SageRows(x.data_ptr(), s[0], s[2], s[1])
 
 
-def _check_rows(name: str, x: torch.Tensor, like: Optional[torch.Tensor] = None) -> None:
-    if not x.is_cuda:
-        raise ValueError("libsage works on CUDA tensors only")
-    if x.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be float16 or bfloat16")
-    if like is not None and (x.shape != like.shape or x.dtype != like.dtype
-                             or x.device != like.device):
+def _like(name: str, x: torch.Tensor, like: torch.Tensor) -> SageRows:
+    """``_rows`` of a tensor that belongs to ``like``."""
+    if x.shape != like.shape or x.dtype != like.dtype or x.get_device() != like.get_device():
         raise ValueError(f"{name} must have the shape, type and device of the tensor it belongs to")
-    if not _supported(x):
-        raise ValueError(f"{name}: channels must be contiguous and 16-byte aligned, the other "
-                         "strides multiples of 8 elements and at least d")
+    return _rows(x)
+
+
+def _type_and_device(x: torch.Tensor) -> Tuple[int, int]:
+    dev, dtype = x.get_device(), _DTYPES.get(x.dtype)
+    if dev < 0:
+        raise ValueError("libsage works on CUDA tensors only")
+    if dtype is None:
+        raise ValueError("tensors must be float16 or bfloat16")
+    return dtype, dev
 
 
 def _params(q, k, positions, rope: Rope, gains) -> Tuple[SageRopeParams, Optional[int]]:
-    _check_rows("q", q)
-    _check_rows("k", k)
-    B, N, Hq, d = _shape(q)
-    if q.dim() != k.dim() or q.dtype != k.dtype or q.device != k.device:
+    dtype, dev = _type_and_device(q)
+    qs, ks = q.shape, k.shape
+    if len(qs) == 3:
+        B, (N, Hq, d), Hkv = 1, qs, ks[1]
+    elif len(qs) == 4:
+        B, Hq, N, d = qs
+        Hkv = ks[1]
+    else:
+        raise ValueError("q and k must be [T, H, d] or [B, H, N, d]")
+    if len(ks) != len(qs) or q.dtype != k.dtype or k.get_device() != dev:
         raise ValueError("q and k must have one layout, type and device")
-    Bk, Nk, Hkv, dk = _shape(k)
-    if (Bk, Nk, dk) != (B, N, d) or d != rope.d:
+    if (ks[0] != qs[0] or ks[-1] != d or d != rope.d or (len(qs) == 4 and ks[2] != N)):
         raise ValueError("q and k must hold the same tokens, with rope.d channels")
     for g in gains:
         if g is None:
             continue
         if not rope.norm:
             raise ValueError("gains belong to the norm (norm=False takes none)")
-        if (g.dtype != torch.float32 or g.shape != (d,) or g.device != q.device
-                or not g.is_contiguous()):
+        if (g.dtype != torch.float32 or g.shape != (d,) or g.get_device() != dev
+                or g.stride(0) != 1):
             raise ValueError("gains must be contiguous float32 [d] tensors on q's device")
     axis_stride = batch_stride = 0
     bits, ptr = 32, None
     if rope.rotary_dim:
         if positions is None:
             raise ValueError("positions are needed")
-        if positions.dtype not in (torch.int32, torch.int64) or positions.device != q.device:
+        bits = 32 if positions.dtype == torch.int32 else 64
+        if (bits == 64 and positions.dtype != torch.int64) or positions.get_device() != dev:
             raise ValueError("positions must be int32 or int64 on q's device")
-        lead = () if rope.axes == 1 else (rope.axes,)
-        shapes = [lead + (N,)] + ([lead + (B, N)] if q.dim() == 4 else [])
-        if rope.axes == 1:
-            shapes += [(1,) + s for s in shapes]
-        if tuple(positions.shape) not in shapes or not positions.is_contiguous():
-            raise ValueError(f"positions must be contiguous, of shape {shapes[0]}"
-                             + (f" or {shapes[1]}" if q.dim() == 4 else ""))
-        per_axis = positions.numel() // rope.axes
-        axis_stride = per_axis
-        batch_stride = N if per_axis == B * N and B > 1 else 0
-        bits, ptr = (32 if positions.dtype == torch.int32 else 64), positions.data_ptr()
-    prm = SageRopeParams(B, N, Hq, Hkv, d, _DTYPES[q.dtype], int(rope.norm), rope.eps,
-                         rope.rotary_dim, int(rope.interleaved), rope.axes, rope._sections,
-                         ctypes.cast(rope._freq, ctypes.c_void_p), bits, axis_stride,
-                         batch_stride)
+        ps, axes = tuple(positions.shape), rope.axes
+        if axes == 1 and len(ps) > 1 and ps[0] == 1 and ps != (B, N):
+            ps = ps[1:]  # [1, N] or [1, B, N]
+        shared, own = ((N,), (B, N)) if axes == 1 else ((axes, N), (axes, B, N))
+        if (ps != shared and (len(qs) != 4 or ps != own)) or not positions.is_contiguous():
+            raise ValueError(f"positions must be contiguous, of shape {shared}"
+                             + (f" or {own}" if len(qs) == 4 else ""))
+        axis_stride = N if ps == shared else B * N
+        batch_stride = 0 if ps == shared else N
+        ptr = positions.data_ptr()
+    prm = SageRopeParams(B, N, Hq, Hkv, d, dtype, rope.norm, rope.eps,
+                         rope.rotary_dim, rope.interleaved, rope.axes, rope._sections,
+                         rope._freq_ptr, bits, axis_stride, batch_stride)
     return prm, ptr
 
 
@@ -149,11 +149,16 @@ def _ptr(x: Optional[torch.Tensor]) -> Optional[int]:
     return None if x is None else x.data_ptr()
 
 
-def _out(name: str, x: Optional[torch.Tensor], like: torch.Tensor) -> torch.Tensor:
-    if x is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    _check_rows(name, x, like)
-    return x
+def _call(name: str, device: int, *args) -> None:
+    """Calls the library on the tensors' device and its current stream."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device:
+        status = getattr(lib(), name)(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(lib(), name)(*args, stream)
+    if status:
+        check(name, status)
 
 
 def qk_norm_rope_fwd(q, k, positions, rope: Rope, gain_q=None, gain_k=None, q_out=None,
@@ -166,13 +171,12 @@ def qk_norm_rope_fwd(q, k, positions, rope: Rope, gain_q=None, gain_k=None, q_ou
     the caller must not overlap the inputs.
     """
     prm, pos = _params(q, k, positions, rope, (gain_q, gain_k))
-    q_out, k_out = _out("q_out", q_out, q), _out("k_out", k_out, k)
-    if prm.B * prm.N == 0:
-        return q_out, k_out
-    with torch.cuda.device(q.device):
-        check("sage_qk_norm_rope_fwd", lib().sage_qk_norm_rope_fwd(
-            ctypes.byref(prm), _rows(q), _rows(k), _ptr(gain_q), _ptr(gain_k), pos,
-            _rows(q_out), _rows(k_out), _stream(q.device)))
+    q_out = q.new_empty(q.shape) if q_out is None else q_out
+    k_out = k.new_empty(k.shape) if k_out is None else k_out
+    rows_q, rows_k = _like("q_out", q_out, q), _like("k_out", k_out, k)
+    if q.numel():
+        _call("sage_qk_norm_rope_fwd", q.get_device(), prm, _rows(q), _rows(k), _ptr(gain_q),
+              _ptr(gain_k), pos, rows_q, rows_k)
     return q_out, k_out
 
 
@@ -183,27 +187,28 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, rope: Rope, gain_q=None, g
     The gains' gradients are float32 [d] whether or not gains were given (None without norm).
     """
     prm, pos = _params(q, k, positions, rope, (gain_q, gain_k))
-    _check_rows("dq_out", dq_out, q)
-    _check_rows("dk_out", dk_out, k)
-    dq, dk = _out("dq", dq, q), _out("dk", dk, k)
-    dgain = torch.empty((2, rope.d), dtype=torch.float32, device=q.device) if rope.norm else None
-    if prm.B * prm.N == 0:
-        if dgain is None:
-            return dq, dk, None, None
-        dgain.zero_()
-        return dq, dk, dgain[0], dgain[1]
+    dq = q.new_empty(q.shape) if dq is None else dq
+    dk = k.new_empty(k.shape) if dk is None else dk
+    rows = (_like("dq_out", dq_out, q), _like("dk_out", dk_out, k), _like("dq", dq, q),
+            _like("dk", dk, k))
+    dgain_q = dgain_k = None
+    if rope.norm:
+        dgain_q, dgain_k = torch.empty((2, rope.d), dtype=torch.float32, device=q.device)
+    if q.numel() == 0:
+        if rope.norm:
+            dgain_q.zero_()
+            dgain_k.zero_()
+        return dq, dk, dgain_q, dgain_k
     if workspace is None and rope.norm:
-        n = int(lib().sage_qk_norm_rope_workspace_bytes(ctypes.byref(prm)))
+        n = int(lib().sage_qk_norm_rope_workspace_bytes(prm))
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    with torch.cuda.device(q.device):
-        check("sage_qk_norm_rope_bwd", lib().sage_qk_norm_rope_bwd(
-            ctypes.byref(prm), _rows(q), _rows(k), _ptr(gain_q), _ptr(gain_k), pos,
-            _rows(dq_out), _rows(dk_out), _rows(dq), _rows(dk),
-            dgain[0].data_ptr() if rope.norm else None,
-            dgain[1].data_ptr() if rope.norm else None, _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _stream(q.device)))
-    return (dq, dk, dgain[0], dgain[1]) if rope.norm else (dq, dk, None, None)
+    elif workspace is not None and (workspace.get_device() != q.get_device()
+                                    or not workspace.is_contiguous()):
+        raise ValueError("the workspace must be a contiguous tensor on q's device")
+    _call("sage_qk_norm_rope_bwd", q.get_device(), prm, _rows(q), _rows(k), _ptr(gain_q),
+          _ptr(gain_k), pos, *rows, _ptr(dgain_q), _ptr(dgain_k), _ptr(workspace),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
+    return dq, dk, dgain_q, dgain_k
 
 
 class _QkNormRope(torch.autograd.Function):

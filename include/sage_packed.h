@@ -64,7 +64,8 @@ typedef struct {
                               0 gives every batch entry the same positions                 */
 } sage_rope_params;
 
-/* q_out, k_out: rotated q and k.  gain_q, gain_k: float32 [d] (NULL: ones); pos: device.
+/* q_out, k_out: rotated q and k.  gain_q, gain_k: float32 [d], 16-byte
+ * aligned (NULL: ones); pos: device.
  * Reads each row once and writes it once; float32 arithmetic, rounded once. */
 int sage_qk_norm_rope_fwd(const sage_rope_params* p, const sage_rows* q, const sage_rows* k,
                           const float* gain_q, const float* gain_k, const void* pos,
@@ -95,6 +96,7 @@ int sage_qk_norm_rope_bwd(const sage_rope_params* p, const sage_rows* q, const s
 typedef struct {
   int sequences, tiles, pairs, longest; /* longest: tokens of the longest sequence */
   int64_t tokens;                       /* sum of the lengths */
+  int64_t causal_steps, full_steps;     /* (query tile, key tile) pairs of one head */
 } sage_packed_info;
 
 size_t sage_packed_plan_bytes(const int* lengths, int sequences);

@@ -46,6 +46,8 @@ def test_plan(L, lengths):
     assert info.sequences == len(lengths) and info.tokens == sum(lengths) == b.tokens
     assert info.tiles == sum(tiles) and info.longest == max(lengths)
     assert info.pairs == sum((t + 1) // 2 for t in tiles)
+    assert info.causal_steps == sum(t * (t + 1) // 2 for t in tiles)
+    assert info.full_steps == sum(t * t for t in tiles)
     items = b.plan.numpy().view(np.int32).reshape(-1, 4)
     assert len(items) == 2 * (info.tiles + info.pairs) + 1  # never empty
     starts = np.concatenate([[0], np.cumsum(lengths)])
