@@ -224,7 +224,7 @@ float packed_tau(const sage_packed_params* p) {
 
 // 4-D map (channel, row of a tile, token, head) of 16-bit rows: the row and the token axis have
 // the same stride, so a box that starts at a negative row reads zeros there.  The box is 64
-// channels x 128 rows (rows of 128 bytes, swizzled).
+// channels x d rows (rows of 128 bytes, swizzled).
 bool make_tile_map(CUtensorMap* m, const sage_rows* r, const sage_packed_params* p, int heads) {
   auto fn = encode_fn();
   if (!fn) return false;
@@ -233,7 +233,7 @@ bool make_tile_map(CUtensorMap* m, const sage_rows* r, const sage_packed_params*
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(p->d), sage::packed::BT,
                         static_cast<cuuint64_t>(p->T), static_cast<cuuint64_t>(heads)};
   cuuint64_t strides[3] = {ts * 2, ts * 2, hs * 2};
-  cuuint32_t box[4] = {64, sage::packed::BT, 1, 1};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p->d), 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   auto encode = [&] {
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, r->ptr, dims, strides, box, estr,
@@ -365,18 +365,18 @@ int run_packed_bwd(const sage_packed_params* p, const sage_packed_info* info, co
   a.tau = packed_tau(p);
   a.scale_log2 = a.tau * 1.4426950408889634f;
   const int64_t pair_bytes = info->tokens * D * 2 * 2;  // two tensors of one head
+  // dq_kernel first: it refines D for dkv_kernel
+  a.grid = {r.items, info->tiles, p->Hq, grid_chunk(p, info, p->Hq, pair_bytes / r.group)};
+  a.out[0] = packed_out(dq);
+  s = launch_packed(B::dq_kernel<T, D>, B::Cfg<D>::kLaunchRegs, static_cast<int64_t>(info->tiles) * p->Hq,
+                    B::Cfg<D>::kThreads, B::dq_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
+  if (s != SAGE_OK) return s;
   a.grid = {r.items, info->tiles, p->Hkv, grid_chunk(p, info, p->Hkv, pair_bytes * r.group)};
   a.out[0] = packed_out(dv);
   a.out[1] = packed_out(dk);
-  s = launch_packed(B::dkv_kernel<T, D>, B::kLaunchRegs,
-                    static_cast<int64_t>(info->tiles) * p->Hkv, B::kThreads,
-                    B::dkv_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
-  if (s != SAGE_OK) return s;
-  a.grid = {r.items, info->tiles, p->Hq, grid_chunk(p, info, p->Hq, pair_bytes / r.group)};
-  a.out[0] = packed_out(dq);
-  return launch_packed(B::dq_kernel<T, D>, B::kLaunchRegs,
-                       static_cast<int64_t>(info->tiles) * p->Hq, B::kThreads,
-                       B::dq_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
+  return launch_packed(B::dkv_kernel<T, D>, B::Cfg<D>::kLaunchRegs,
+                       static_cast<int64_t>(info->tiles) * p->Hkv, B::Cfg<D>::kThreads,
+                       B::dkv_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
 }
 
 }  // namespace

@@ -5,17 +5,27 @@
 // (h over the query heads that share j's key head).  Tiles and tensor maps as in the forward.
 //
 // Two kernels after the row pass that forms D, each recomputing S and dP for its own direction:
+//   * dq_kernel: one CTA per (query tile, query head), walking the key tiles: dQ += dS K;
 //   * dkv_kernel: one CTA per (key tile, key head), walking the query tiles of every head of the
 //     group.  It works on transposed tiles (rows = keys), so P^T and dS^T go from registers to
-//     TMEM as the A operands of dV += P^T dO and dK += dS^T Q, and dV, dK stay in TMEM;
-//   * dq_kernel: one CTA per (query tile, query head), walking the key tiles: dQ += dS K.
+//     TMEM as the A operands of dV += P^T dO and dK += dS^T Q, and dV, dK stay in TMEM.
 // Seven products where one fused pass would need five, but no gradient is ever added up across
 // CTAs: no atomics, no float32 accumulator in HBM, no finishing pass, the same bits every run,
 // and grouped heads cost nothing extra.
 //
-// Both: warps 0-7 compute (a thread holds half a row, 64 columns: warps 0-3 the first half),
-// warp 8 TMA producer, warp 9 MMA issuer, warps 10-11 complete the warpgroup; in dkv_kernel warp
-// 10 brings the query rows' LSE and D to shared memory.
+// Both work on blocks of 128 rows x D columns (the walked side in runs of D rows).  d = 128 fills
+// TMEM and shared memory: one CTA per SM.  d = 64 takes half of both, so two CTAs share an SM and
+// hide each other's latencies, their first loads and last stores included.
+// A thread holds 64 columns of a row: warps 0-3 (d = 128: 0-7, the second four with the second
+// half of the columns) compute; then follow the TMA producer, the MMA issuer, a warp that brings
+// the query rows' LSE and D to shared memory (dkv_kernel), and an idle one that completes the
+// warpgroup, which gives registers to the computing ones.
+//
+// D_i: the row pass takes it from the stored, rounded o.  That rounding weighs most in rows of few
+// keys (|o| ~ |v|), so rows of a sequence's first tile get it from P and dP instead: dq_kernel
+// walks their at most 128 keys twice, first for D_i = sum_j P_ij dP_ij, which dkv_kernel then
+// uses too.  (bf16, 1024-token documents: dQ and dK off by 0.24% of their norm, not 0.26%; their
+// two unavoidable roundings make 0.235%.)
 //
 // Rounding: P and dS to the tensors' type for their products; sums in float32; outputs once.
 // Half precision: P is multiplied by 2^14 before it is rounded, and dS by the power of two that
@@ -30,11 +40,21 @@ namespace sage {
 namespace packed {
 namespace bwd {
 
-constexpr int kThreads = 384;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kRowWarp = 10;
-constexpr int kLaunchRegs = 168, kComputeRegs = 216, kOtherRegs = 72;
-static_assert(256 * kComputeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
-              "register split exceeds the launch allocation");
+template <int D>
+struct Cfg {
+  static constexpr int BN = D;                   // rows of the walked side per step
+  static constexpr int kWG = BN / 64;            // computing warpgroups
+  static constexpr int kCompute = 128 * kWG;
+  static constexpr int kThreads = kCompute + 128;
+  static constexpr int kProducerWarp = 4 * kWG, kMmaWarp = kProducerWarp + 1,
+                       kRowWarp = kProducerWarp + 2;
+  static constexpr int kCtas = D == 64 ? 2 : 1;  // per SM
+  static constexpr int kLaunchRegs = D == 64 ? 128 : 168;
+  static constexpr int kComputeRegs = D == 64 ? 184 : 216, kOtherRegs = 72;
+  static constexpr int kTmem = 4 * D;            // columns
+  static_assert(kCompute * kComputeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
+                "register split exceeds the launch allocation");
+};
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <typename T>
@@ -128,18 +148,19 @@ __device__ __forceinline__ float ds_factor(const uint32_t* norms) {
   return scalbnf(1.0f, e);
 }
 
-// D (+)= A B over the BT rows of tile B, A in TMEM: 32 columns at a_tmem and 32 at a_tmem + 64.
+// D (+)= A B over the 64 WG rows of tile B, A in TMEM: 32 columns from every 64th.
+template <int WG>
 __device__ __forceinline__ void mma_sum(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
                                         uint32_t idesc, bool start) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < WG; ++h)
     mma_sum_half(d_tmem, a_tmem + 64 * h, b + step_mn(4 * h), idesc, start && h == 0);
 }
 
 struct Args {
   Grid grid;          // heads: query heads (dq_kernel), key heads (dkv_kernel)
   const float* lse;   // [Hq][T]
-  const float* dvec;  // [Hq][T]
+  float* dvec;        // [Hq][T]
   const uint32_t* norms;
   Out out[2];         // dq_kernel: dq; dkv_kernel: dv, dk
   int64_t T;
@@ -150,7 +171,7 @@ struct Args {
 
 // P (times 2^shift) of 64 columns from the scores x, in place: z = x c - shift(e).
 // MASK: columns for which hidden(e) holds are zero.
-template <bool MASK, typename Shift, typename Hidden>
+template <bool MASK, bool POLY, typename Shift, typename Hidden>
 __device__ __forceinline__ void probabilities(uint32_t (&x)[2][32], float c, Shift shift,
                                               Hidden hidden) {
   const float2 c2 = make_float2(c, c);
@@ -164,7 +185,7 @@ __device__ __forceinline__ void probabilities(uint32_t (&x)[2][32], float c, Shi
       if (hidden(e)) z.x = -INFINITY;
       if (hidden(e + 1)) z.y = -INFINITY;
       p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-    } else if (poly_pair(e >> 1)) {
+    } else if (POLY && (e & 7) == 6) {
       p = exp2_fma2(z);
     } else {
       p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
@@ -177,12 +198,13 @@ __device__ __forceinline__ void probabilities(uint32_t (&x)[2][32], float c, Shi
 // ---- dK and dV ------------------------------------------------------------------------------
 template <typename T, int D>
 struct DkvSmem {
-  static constexpr int NST = D == 128 ? 4 : 8;  // Q / dO tiles in flight
+  static constexpr int BN = Cfg<D>::BN;
+  static constexpr int NST = D == 128 ? 4 : 6;  // Q / dO runs in flight
   alignas(1024) T k[BT * D];
   alignas(1024) T v[BT * D];
-  alignas(1024) T ring[NST][BT * D];
-  alignas(16) float lse[2][BT];   // LSE log2 e - P's shift of the query tile's rows, +inf: padding
-  alignas(16) float dvec[2][BT];
+  alignas(1024) T ring[NST][BN * D];
+  alignas(16) float lse[2][BN];  // LSE log2 e - P's shift of the query rows, +inf: padding
+  alignas(16) float dvec[2][BN];
   uint64_t kv_full, full[NST], empty[NST], vec_full[2], vec_empty[2];
   uint64_t s_full, dp_full, p_ready, ds_ready, done;
   uint32_t tmem_base;
@@ -192,40 +214,44 @@ template <typename T, int D>
 constexpr size_t dkv_smem_bytes() {
   return sizeof(DkvSmem<T, D>) + 1024;
 }
-static_assert(dkv_smem_bytes<__half, 128>() <= 232448, "shared memory exceeds the limit");
-
-// TMEM columns: S^T (then P^T), dP^T (then dS^T), dV, dK.  P^T and dS^T of column half h start
-// at 64 h of their tile, over columns that only the same warps have read.
-constexpr uint32_t kColDP = 128, kColDV = 256, kColDK = 384;
+static_assert(dkv_smem_bytes<__half, 128>() <= 232448 && dkv_smem_bytes<__half, 64>() <= 115712,
+              "shared memory exceeds the limit");
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                const Args a) {
   extern __shared__ uint8_t smem_raw[];
   using SM = DkvSmem<T, D>;
+  using C = Cfg<D>;
   SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-  constexpr int NST = SM::NST;
+  constexpr int NST = SM::NST, BN = C::BN;
+  // TMEM columns: S^T (then P^T), dP^T (then dS^T), dV, dK.  P^T and dS^T of column half h start at
+  // 64 h of their block, over columns that only the same warps have read.
+  constexpr uint32_t kColDP = BN, kColDV = 2 * BN, kColDK = 2 * BN + D;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int kv_head;
   const Item it = grid_at(a.grid, kv_head);
   const int tiles = tiles_of(it);
   // under a causal mask the list's order (most work first) is by query tile: mirrored for keys
   const int kt = a.causal ? tiles - 1 - it.tile : it.tile;
-  const int first = a.causal ? kt : 0;          // first query tile that sees these keys
-  const int n_all = (tiles - first) * a.group;
-  // the steps' (query head, query tile), in order
+  const int runs = tiles * (BT / BN), pad = tiles * BT - it.len;
+  // first run of query rows that sees these keys and is not all padding
+  const int diag = kt * (BT / BN);
+  const int first = max(a.causal ? diag : 0, pad / BN);
+  const int n_all = (runs - first) * a.group;
+  // the steps' (query head, run of query rows), in order
   struct Walk {
-    int head, tile, first, tiles;
+    int head, run, first, runs;
     __device__ __forceinline__ void next() {
-      if (++tile == tiles) {
-        tile = first;
+      if (++run == runs) {
+        run = first;
         ++head;
       }
     }
   };
-  const Walk begin = {kv_head * a.group, first, first, tiles};
+  const Walk begin = {kv_head * a.group, first, first, runs};
 
   if (threadIdx.x == 0) {
     sm.abort = device_aborted() ? 1 : 0;
@@ -236,19 +262,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.vec_full[s], 32);
-      mbar_init(&sm.vec_empty[s], 256);
+      mbar_init(&sm.vec_empty[s], C::kCompute);
     }
     mbar_init(&sm.s_full, 1);
     mbar_init(&sm.dp_full, 1);
-    mbar_init(&sm.p_ready, 256);
-    mbar_init(&sm.ds_ready, 256);
+    mbar_init(&sm.p_ready, C::kCompute);
+    mbar_init(&sm.ds_ready, C::kCompute);
     mbar_init(&sm.done, 1);
     fence_barrier_init();
   }
   __syncthreads();
   if (sm.abort) return;
-  if (warp == kMmaWarp) {
-    tmem_alloc(&sm.tmem_base, 512);
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&sm.tmem_base, C::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -256,52 +282,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-    if (warp == kProducerWarp) {
+  if (warp >= C::kProducerWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
+    if (warp == C::kProducerWarp) {
       if (lane == 0) {
         mbar_arrive_expect_tx(&sm.kv_full, 2 * BT * D * 2);
-        load_tile<T, D>(sm.k, &tm_k, tile_at(it, kt), kv_head, &sm.kv_full);
-        load_tile<T, D>(sm.v, &tm_v, tile_at(it, kt), kv_head, &sm.kv_full);
+        load_tile<T, D, BN, BT>(sm.k, &tm_k, it, kt, kv_head, &sm.kv_full);
+        load_tile<T, D, BN, BT>(sm.v, &tm_v, it, kt, kv_head, &sm.kv_full);
         Ring<NST> ring;
         Walk at = begin;
         for (int n = 0; n < n_all; ++n, at.next()) {  // Q0 dO0 Q1 dO1 ...
-          const TileAt t = tile_at(it, at.tile);
 #pragma unroll
           for (int w = 0; w < 2; ++w, ring.next()) {
             const int st = ring.slot;
             if (2 * n + w >= NST) mbar_wait(&sm.empty[st], ring.parity ^ 1, 401);
-            mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
-            load_tile<T, D>(sm.ring[st], w ? &tm_do : &tm_q, t, at.head, &sm.full[st]);
+            mbar_arrive_expect_tx(&sm.full[st], BN * D * 2);
+            load_tile<T, D, BN, BN>(sm.ring[st], w ? &tm_do : &tm_q, it, at.run, at.head,
+                                    &sm.full[st]);
           }
         }
       }
       __syncwarp();
-    } else if (warp == kRowWarp) {
+    } else if (warp == C::kRowWarp) {
       Walk at = begin;
       for (int n = 0; n < n_all; ++n, at.next()) {
         const int b = n & 1;
         if (n >= 2) mbar_wait(&sm.vec_empty[b], ((n >> 1) - 1) & 1, 402);
         const int64_t base = at.head * a.T + it.start;
 #pragma unroll
-        for (int r = lane; r < BT; r += 32) {
-          const int i = row_index(it, at.tile, r);
+        for (int r = lane; r < BN; r += 32) {
+          const int i = row_index<BN>(it, at.run, r);
           sm.lse[b][r] = i >= 0 ? fmaf(a.lse[base + i], kLog2e, -Scaling<T>::kPShift) : INFINITY;
           sm.dvec[b][r] = i >= 0 ? a.dvec[base + i] : 0.0f;
         }
         mbar_arrive(&sm.vec_full[b]);
       }
       __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == C::kMmaWarp) {
       if (lane == 0) {
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-        constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
+        constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
         constexpr uint32_t id_g = instr_desc(1, kFmt, kFmt, false, true, BT, D);
         const uint64_t k_desc = desc_k(sm.k), v_desc = desc_k(sm.v);
         auto product = [&](uint32_t col, uint64_t rows, const Ring<NST>& at, uint64_t* bar) {
           mbar_wait(&sm.full[at.slot], at.parity, 411);
           tc_fence_after();
-          mma_rows<D>(tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
+          mma_rows<D, BN>(tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
           mma_commit(bar);
         };
         Ring<NST> q_at, do_at;  // of Q_n and dO_n
@@ -319,13 +345,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait(&sm.p_ready, n & 1, 412);
           tc_fence_after();
           // dV += P^T dO
-          mma_sum(tmem + kColDV, tmem, desc_mn(sm.ring[do_slot]), id_g, n == 0);
+          mma_sum<C::kWG>(tmem + kColDV, tmem, desc_mn<BN>(sm.ring[do_slot]), id_g, n == 0);
           mma_commit(&sm.empty[do_slot]);
           if (more) product(0, k_desc, q_at, &sm.s_full);
           mbar_wait(&sm.ds_ready, n & 1, 413);
           tc_fence_after();
           // dK += dS^T Q
-          mma_sum(tmem + kColDK, tmem + kColDP, desc_mn(sm.ring[q_slot]), id_g, n == 0);
+          mma_sum<C::kWG>(tmem + kColDK, tmem + kColDP, desc_mn<BN>(sm.ring[q_slot]), id_g, n == 0);
           mma_commit(&sm.empty[q_slot]);
           if (more) product(kColDP, v_desc, do_at, &sm.dp_full);
         }
@@ -334,11 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     tc_fence_before();
-    named_barrier_sync(15, kThreads);
+    named_barrier_sync(15, C::kThreads);
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmem);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kComputeRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kComputeRegs));
     const int half = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // key row of the tile
     const uint32_t lane_base = tmem + (((warp & 3) * 32u) << 16);
@@ -349,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       factor = ds_factor(a.norms + (static_cast<int64_t>(it.seq) * a.grid.heads + kv_head) * 2);
     const float f_ds = factor * exp2f(-Scaling<T>::kPShift);
 
-    auto step = [&](int n, auto masked) {
+    auto step = [&](int n, int run, auto masked) {
       constexpr bool MASK = decltype(masked)::value;
       const int b = n & 1;
       uint32_t x[2][32];
@@ -361,14 +387,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_wait_regs32(x[0]);
       tie32(x[1]);
       const float* lse = sm.lse[b] + 64 * half;
-      // query column below the key row's own position: hidden (diagonal tile of a causal mask)
-      probabilities<MASK>(
+      // query row before the key's own position: hidden (the diagonal of a causal mask)
+      const int hidden = r - (run - diag) * BN - 64 * half;  // columns below it
+      probabilities<MASK, true>(
           x, c,
           [&](int e) {
             const float2 s = *reinterpret_cast<const float2*>(lse + e);
             return make_float2(-s.x, -s.y);
           },
-          [&](int e) { return 64 * half + e < r; });
+          [&](int e) { return e < hidden; });
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[16];
@@ -383,23 +410,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // dS = P (dP - D)
       mbar_wait(&sm.dp_full, n & 1, 422);
       tc_fence_after();
-      uint32_t y[2][32];
-      tmem_ld32(dp_at, y[0]);
-      tmem_ld32(dp_at + 32, y[1]);
-      tmem_ld_wait_regs32(y[0]);
-      tie32(y[1]);
       const float* dv = sm.dvec[b] + 64 * half;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w[16];
+        uint32_t y[32], w[16];
+        tmem_ld32(dp_at + 32 * h, y);
+        tmem_ld_wait_regs32(y);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float2 d2 = *reinterpret_cast<const float2*>(dv + 32 * h + 2 * e);
           float2 p = make_float2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1]));
           if (Scaling<T>::kOn) p = __fmul2_rn(p, make_float2(f_ds, f_ds));
           const float2 t =
-              __fadd2_rn(make_float2(__uint_as_float(y[h][2 * e]),
-                                     __uint_as_float(y[h][2 * e + 1])),
+              __fadd2_rn(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])),
                          make_float2(-d2.x, -d2.y));
           const float2 s = __fmul2_rn(p, t);
           w[e] = Cvt<T>::pack2(s.x, s.y);
@@ -413,47 +436,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Walk at = begin;
     for (int n = 0; n < n_all; ++n, at.next()) {
-      if (a.causal && at.tile == kt)
-        step(n, std::true_type{});
+      if (a.causal && at.run < diag + BT / BN)
+        step(n, at.run, std::true_type{});
       else
-        step(n, std::false_type{});
+        step(n, at.run, std::false_type{});
     }
     mbar_wait(&sm.done, 0, 423);
     tc_fence_after();
-    // warps 0-3 store dV, warps 4-7 dK
+    // dV and dK: by a warpgroup each, or one after the other
     const int i = row_index(it, kt, r);
-    const uint32_t g_at = lane_base + (half == 0 ? kColDV : kColDK);
-    const float scale = half == 0 ? exp2f(-Scaling<T>::kPShift) : a.tau / factor;
-    const Out& out = a.out[half];
-    T* dst = reinterpret_cast<T*>(out.ptr) + (static_cast<int64_t>(it.start) + i) * out.ts +
-             kv_head * out.hs;
 #pragma unroll
-    for (int cc = 0; cc < D; cc += 32) {
-      uint32_t y[32];
-      tmem_ld32(g_at + cc, y);
-      tmem_ld_wait_regs32(y);
-      if (i >= 0) {
+    for (int w = 0; w < 2 / C::kWG; ++w) {
+      const int which = C::kWG == 2 ? half : w;
+      const uint32_t g_at = lane_base + (which == 0 ? kColDV : kColDK);
+      const float scale = which == 0 ? exp2f(-Scaling<T>::kPShift) : a.tau / factor;
+      const Out& out = a.out[which];
+      T* dst = reinterpret_cast<T*>(out.ptr) + (static_cast<int64_t>(it.start) + i) * out.ts +
+               kv_head * out.hs;
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          float f[8];
+      for (int cc = 0; cc < D; cc += 32) {
+        uint32_t y[32];
+        tmem_ld32(g_at + cc, y);
+        tmem_ld_wait_regs32(y);
+        if (i >= 0) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * scale;
-          *reinterpret_cast<uint4*>(dst + cc + e) = pack8<T>(f);
+          for (int e = 0; e < 32; e += 8) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * scale;
+            *reinterpret_cast<uint4*>(dst + cc + e) = pack8<T>(f);
+          }
         }
       }
     }
     tc_fence_before();
-    named_barrier_sync(15, kThreads);
+    named_barrier_sync(15, C::kThreads);
   }
 }
 
 // ---- dQ -------------------------------------------------------------------------------------
 template <typename T, int D>
 struct DqSmem {
-  static constexpr int NST = D == 128 ? 5 : 8;  // K / V tiles in flight
+  static constexpr int BN = Cfg<D>::BN;
+  static constexpr int NST = D == 128 ? 5 : 8;  // K / V runs in flight
   alignas(1024) T q[BT * D];
   alignas(1024) T dout[BT * D];
-  alignas(1024) T ring[NST][BT * D];
+  alignas(1024) T ring[NST][BN * D];
+  float dot[2][BT];  // halves of D, where the row pass's is replaced
   uint64_t q_full, full[NST], empty[NST], s_full[2], dp_full, dp_free, ds_ready, done;
   uint32_t tmem_base;
   int abort;
@@ -462,26 +491,33 @@ template <typename T, int D>
 constexpr size_t dq_smem_bytes() {
   return sizeof(DqSmem<T, D>) + 1024;
 }
-static_assert(dq_smem_bytes<__half, 128>() <= 232448, "shared memory exceeds the limit");
-
-// TMEM columns: two S tiles (dS overwrites the one it came from) at 0 and 128, dP, dQ.
-constexpr uint32_t kColQdP = 256, kColQdQ = 384;
+static_assert(dq_smem_bytes<__half, 128>() <= 232448 && dq_smem_bytes<__half, 64>() <= 115712,
+              "shared memory exceeds the limit");
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
               const Args a) {
   extern __shared__ uint8_t smem_raw[];
   using SM = DqSmem<T, D>;
+  using C = Cfg<D>;
   SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-  constexpr int NST = SM::NST;
+  constexpr int NST = SM::NST, BN = C::BN;
+  // TMEM columns: two S blocks (dS overwrites the one it came from), dP, dQ
+  constexpr uint32_t kColDP = 2 * BN, kColDQ = 3 * BN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int head;
   const Item it = grid_at(a.grid, head);
   const int kv_head = head / a.group;
-  const int tiles = tiles_of(it);
-  const int n_all = a.causal ? it.tile + 1 : tiles;
+  const int tiles = tiles_of(it), pad = tiles * BT - it.len;
+  // the steps' runs of keys: first .. first + runs - 1, in a sequence's first tile (or only one)
+  // twice, the first `pre` steps for D
+  const int first = pad / BN;
+  const int runs = (a.causal ? it.tile + 1 : tiles) * (BT / BN) - first;
+  const int pre = runs * BN <= BT ? runs : 0;
+  const int n_all = pre + runs;
+  auto run_of = [&](int n) { return first + (n < pre ? n : n - pre); };
 
   if (threadIdx.x == 0) {
     sm.abort = device_aborted() ? 1 : 0;
@@ -493,15 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.s_full[0], 1);
     mbar_init(&sm.s_full[1], 1);
     mbar_init(&sm.dp_full, 1);
-    mbar_init(&sm.dp_free, 256);
-    mbar_init(&sm.ds_ready, 256);
+    mbar_init(&sm.dp_free, C::kCompute);
+    mbar_init(&sm.ds_ready, C::kCompute);
     mbar_init(&sm.done, 1);
     fence_barrier_init();
   }
   __syncthreads();
   if (sm.abort) return;
-  if (warp == kMmaWarp) {
-    tmem_alloc(&sm.tmem_base, 512);
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&sm.tmem_base, C::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -509,68 +545,72 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-    if (warp == kProducerWarp) {
+  if (warp >= C::kProducerWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
+    if (warp == C::kProducerWarp) {
       if (lane == 0) {
         mbar_arrive_expect_tx(&sm.q_full, 2 * BT * D * 2);
-        load_tile<T, D>(sm.q, &tm_q, tile_at(it, it.tile), head, &sm.q_full);
-        load_tile<T, D>(sm.dout, &tm_do, tile_at(it, it.tile), head, &sm.q_full);
+        load_tile<T, D, BN, BT>(sm.q, &tm_q, it, it.tile, head, &sm.q_full);
+        load_tile<T, D, BN, BT>(sm.dout, &tm_do, it, it.tile, head, &sm.q_full);
         Ring<NST> ring;
-        for (int i = 0; i < 2 * n_all; ++i, ring.next()) {  // K0 V0 K1 V1 ...
-          const int st = ring.slot;
-          if (i >= NST) mbar_wait(&sm.empty[st], ring.parity ^ 1, 501);
-          mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
-          load_tile<T, D>(sm.ring[st], (i & 1) ? &tm_v : &tm_k, tile_at(it, i >> 1), kv_head,
-                          &sm.full[st]);
+        for (int n = 0; n < n_all; ++n) {  // K0 V0 K1 V1 ...
+#pragma unroll
+          for (int w = 0; w < 2; ++w, ring.next()) {
+            const int st = ring.slot;
+            if (2 * n + w >= NST) mbar_wait(&sm.empty[st], ring.parity ^ 1, 501);
+            mbar_arrive_expect_tx(&sm.full[st], BN * D * 2);
+            load_tile<T, D, BN, BN>(sm.ring[st], w ? &tm_v : &tm_k, it, run_of(n), kv_head,
+                                    &sm.full[st]);
+          }
         }
       }
       __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == C::kMmaWarp) {
       if (lane == 0) {
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-        constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
+        constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
         constexpr uint32_t id_g = instr_desc(1, kFmt, kFmt, false, true, BT, D);
         const uint64_t q_desc = desc_k(sm.q), do_desc = desc_k(sm.dout);
         auto product = [&](uint32_t col, uint64_t rows, const Ring<NST>& at, uint64_t* bar) {
           mbar_wait(&sm.full[at.slot], at.parity, 511);
           tc_fence_after();
-          mma_rows<D>(tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
+          mma_rows<D, BN>(tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
           mma_commit(bar);
         };
         Ring<NST> s_at, v_at, k_at;  // K of the next S, V of the next dP, K of the next dQ
         v_at.next();
         mbar_wait(&sm.q_full, 0, 510);
         product(0, q_desc, s_at, &sm.s_full[0]);
-        product(kColQdP, do_desc, v_at, &sm.dp_full);
+        product(kColDP, do_desc, v_at, &sm.dp_full);
         mma_commit(&sm.empty[v_at.slot]);
         s_at.next();
         s_at.next();
         v_at.next();
         v_at.next();
         if (n_all > 1) {
-          product(128, q_desc, s_at, &sm.s_full[1]);
+          product(BN, q_desc, s_at, &sm.s_full[1]);
           s_at.next();
           s_at.next();
         }
-        for (int j = 0; j < n_all; ++j) {
-          if (j + 1 < n_all) {  // dP of the next key tile once this one's has been read
-            mbar_wait(&sm.dp_free, j & 1, 512);
-            product(kColQdP, do_desc, v_at, &sm.dp_full);
+        for (int n = 0; n < n_all; ++n) {
+          if (n + 1 < n_all) {  // dP of the next run once this one's has been read
+            mbar_wait(&sm.dp_free, n & 1, 512);
+            product(kColDP, do_desc, v_at, &sm.dp_full);
             mma_commit(&sm.empty[v_at.slot]);
             v_at.next();
             v_at.next();
           }
-          mbar_wait(&sm.ds_ready, j & 1, 513);
+          mbar_wait(&sm.ds_ready, n & 1, 513);
           tc_fence_after();
           // dQ += dS K
-          mma_sum(tmem + kColQdQ, tmem + 128 * (j & 1), desc_mn(sm.ring[k_at.slot]), id_g,
-                        j == 0);
+          if (n >= pre)
+            mma_sum<C::kWG>(tmem + kColDQ, tmem + BN * (n & 1), desc_mn<BN>(sm.ring[k_at.slot]),
+                            id_g, n == pre);
           mma_commit(&sm.empty[k_at.slot]);
           k_at.next();
           k_at.next();
-          if (j + 2 < n_all) {
-            product(128 * (j & 1), q_desc, s_at, &sm.s_full[j & 1]);
+          if (n + 2 < n_all) {
+            product(BN * (n & 1), q_desc, s_at, &sm.s_full[n & 1]);
             s_at.next();
             s_at.next();
           }
@@ -580,11 +620,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     tc_fence_before();
-    named_barrier_sync(15, kThreads);
+    named_barrier_sync(15, C::kThreads);
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmem);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kComputeRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kComputeRegs));
     const int half = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // query row of the tile
     const uint32_t lane_base = tmem + (((warp & 3) * 32u) << 16);
@@ -593,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // padding rows: P = exp2(-inf) = 0
     const float shift =
         i >= 0 ? fmaf(a.lse[head * a.T + row], kLog2e, -Scaling<T>::kPShift) : INFINITY;
-    const float dvec = i >= 0 ? a.dvec[head * a.T + row] : 0.0f;
+    float dvec = i >= 0 && pre == 0 ? a.dvec[head * a.T + row] : 0.0f;
     const float c = a.scale_log2;
     float factor = 1.0f;
     if (Scaling<T>::kOn)
@@ -601,41 +641,66 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.norms + (static_cast<int64_t>(it.seq) * (a.grid.heads / a.group) + kv_head) * 2);
     const float f_ds = factor * exp2f(-Scaling<T>::kPShift);
 
-    auto step = [&](int j, auto masked) {
+    auto step = [&](int n, auto masked) {
       constexpr bool MASK = decltype(masked)::value;
-      const uint32_t s_at = lane_base + 128 * (j & 1) + 64 * half;
-      const uint32_t dp_at = lane_base + kColQdP + 64 * half;
+      const uint32_t s_at = lane_base + BN * (n & 1) + 64 * half;
+      const uint32_t dp_at = lane_base + kColDP + 64 * half;
       uint32_t x[2][32];
-      mbar_wait(&sm.s_full[j & 1], (j >> 1) & 1, 520);
+      mbar_wait(&sm.s_full[n & 1], (n >> 1) & 1, 520);
       tc_fence_after();
       tmem_ld32(s_at, x[0]);
       tmem_ld32(s_at + 32, x[1]);
       tmem_ld_wait_regs32(x[0]);
       tie32(x[1]);
-      const int key0 = row_index(it, j, 64 * half);
+      const int key0 = row_index<BN>(it, run_of(n), 64 * half);
       const int last = a.causal ? i : 0x7fffffff;
-      probabilities<MASK>(
+      probabilities<MASK, false>(
           x, c, [&](int) { return make_float2(-shift, -shift); },
           [&](int e) { return key0 + e < 0 || key0 + e > last; });
-      mbar_wait(&sm.dp_full, j & 1, 521);
+      mbar_wait(&sm.dp_full, n & 1, 521);
       tc_fence_after();
-      uint32_t y[2][32];
-      tmem_ld32(dp_at, y[0]);
-      tmem_ld32(dp_at + 32, y[1]);
-      tmem_ld_wait_regs32(y[0]);
-      tie32(y[1]);
-      tc_fence_before();
-      mbar_arrive(&sm.dp_free);
+      if (n < pre) {  // D += P dP
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t y[32];
+          tmem_ld32(dp_at + 32 * h, y);
+          tmem_ld_wait_regs32(y);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            sum = __ffma2_rn(make_float2(__uint_as_float(x[h][e]), __uint_as_float(x[h][e + 1])),
+                             make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), sum);
+        }
+        tc_fence_before();
+        mbar_arrive(&sm.dp_free);
+        mbar_arrive(&sm.ds_ready);
+        dvec += (sum.x + sum.y) * exp2f(-Scaling<T>::kPShift);
+        if (n == pre - 1) {
+          if (C::kWG == 2) {
+            sm.dot[half][r] = dvec;
+            named_barrier_sync(1, C::kCompute);
+            dvec = sm.dot[0][r] + sm.dot[1][r];
+          }
+          if (half == 0 && i >= 0) a.dvec[head * a.T + row] = dvec;
+        }
+        return;
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w[16];
+        uint32_t y[32], w[16];
+        tmem_ld32(dp_at + 32 * h, y);
+        tmem_ld_wait_regs32(y);
+        if (h == 1) {
+          tc_fence_before();
+          mbar_arrive(&sm.dp_free);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float2 p = make_float2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1]));
           if (Scaling<T>::kOn) p = __fmul2_rn(p, make_float2(f_ds, f_ds));
-          const float2 t = __fadd2_rn(make_float2(__uint_as_float(y[h][2 * e]),
-                                                  __uint_as_float(y[h][2 * e + 1])),
-                                      make_float2(-dvec, -dvec));
+          const float2 t =
+              __fadd2_rn(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])),
+                         make_float2(-dvec, -dvec));
           const float2 s = __fmul2_rn(p, t);
           w[e] = Cvt<T>::pack2(s.x, s.y);
         }
@@ -645,22 +710,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(&sm.ds_ready);
     };
-    const bool ragged = tiles * BT != it.len;
-    for (int j = 0; j < n_all; ++j) {
-      if ((j == 0 && ragged) || (a.causal && j == it.tile))
-        step(j, std::true_type{});
+    for (int n = 0; n < n_all; ++n) {
+      const int run = run_of(n);
+      if ((run == first && pad > 0) || (a.causal && run >= it.tile * (BT / BN)))
+        step(n, std::true_type{});
       else
-        step(j, std::false_type{});
+        step(n, std::false_type{});
     }
     mbar_wait(&sm.done, 0, 522);
     tc_fence_after();
-    // warps 0-3 store the first half of the channels, warps 4-7 the second
+    // a warpgroup stores its part of the channels
     const float scale = a.tau / factor;
     T* dst = reinterpret_cast<T*>(a.out[0].ptr) + row * a.out[0].ts + head * a.out[0].hs;
 #pragma unroll
-    for (int cc = half * (D / 2); cc < (half + 1) * (D / 2); cc += 32) {
+    for (int k0 = 0; k0 < D / C::kWG; k0 += 32) {
+      const int cc = half * (D / C::kWG) + k0;
       uint32_t y[32];
-      tmem_ld32(lane_base + kColQdQ + cc, y);
+      tmem_ld32(lane_base + kColDQ + cc, y);
       tmem_ld_wait_regs32(y);
       if (i >= 0) {
 #pragma unroll
@@ -673,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     tc_fence_before();
-    named_barrier_sync(15, kThreads);
+    named_barrier_sync(15, C::kThreads);
   }
 }
 

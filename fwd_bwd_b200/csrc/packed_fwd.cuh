@@ -16,11 +16,12 @@
 //   warp 8          TMA producer: the query tiles, then K and V tiles through a ring
 //   warp 9          MMA issuer: S = Q K^T (operands in shared memory), O += P V (P in TMEM)
 //   warps 10-11     idle (they complete the warpgroup that gives its registers away)
-// TMEM: S of tile g at 128 g (P overwrites its first 64 columns, two 16-bit values each), O of
-// tile g at 256 + 128 g, accumulated there over all keys.
-// The tensor core alternates between the tiles: while tile 0's softmax runs, it multiplies tile
-// 1's P V and Q K^T.  S of the next key tile is issued after P V of this one, so its arrival
-// also tells the softmax warps that O is up to date.
+// TMEM: S of tile g at 128 g, O of tile g at 256 + D g, accumulated there over all keys.
+//   d = 128 fills TMEM: P (two 16-bit values to a column) overwrites the first half of its S, so S
+//   of the next key tile is issued after P V of this one; the tensor core alternates between the
+//   tiles: while tile 0's softmax runs, it multiplies tile 1's P V and Q K^T.
+//   d = 64 leaves room for P of its own (at 384 + 64 g): S of the next key tile is issued as soon
+//   as this one has been read, and waits for the softmax warps instead of the reverse.
 // The running maximum that P is taken against is raised (and O rescaled in TMEM) only when a
 // row's maximum grows by more than 2^8: P then stays below 256, exact in the final division
 // by the row sum, and most key tiles leave O untouched.
@@ -75,29 +76,36 @@ struct Out {
   int64_t ts, hs;  // elements
 };
 
-// Row and token coordinates of tile t in the 4-D maps.
+// Row and token coordinates of the t-th run of R rows in the 4-D maps.
 struct TileAt {
   int row, token;
 };
+template <int R>
 __device__ __forceinline__ TileAt tile_at(const Item& it, int t) {
-  const int pad = tiles_of(it) * BT - it.len;
+  const int first = t * R - (tiles_of(it) * BT - it.len);  // negative: padding
   TileAt a;
-  a.row = t == 0 ? -pad : 0;
-  a.token = it.start + (t == 0 ? 0 : t * BT - pad);
+  a.row = min(first, 0);
+  a.token = it.start + max(first, 0);
   return a;
 }
-// Index within the sequence of row r of tile t (negative: padding).
+// Index within the sequence of row r of the t-th run of R rows (negative: padding).
+template <int R = BT>
 __device__ __forceinline__ int row_index(const Item& it, int t, int r) {
-  return (t - tiles_of(it)) * BT + it.len + r;
+  return t * R - tiles_of(it) * BT + it.len + r;
 }
 
-// Loads one tile of BT rows: D / 64 boxes of 64 channels (128-byte swizzled rows).
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(T* dst, const CUtensorMap* map, TileAt at, int head,
-                                          uint64_t* bar) {
+// Loads tile t of N rows by boxes of BOX rows x 64 channels (128-byte swizzled rows; the tile's
+// 64-channel parts follow each other).
+template <typename T, int D, int BOX, int N>
+__device__ __forceinline__ void load_tile(T* dst, const CUtensorMap* map, const Item& it, int t,
+                                          int head, uint64_t* bar) {
 #pragma unroll
-  for (int b = 0; b < D / 64; ++b)
-    tma_load_4d(dst + b * BT * 64, map, b * 64, at.row, at.token, head, bar);
+  for (int s = 0; s < N / BOX; ++s) {
+    const TileAt at = tile_at<BOX>(it, t * (N / BOX) + s);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b)
+      tma_load_4d(dst + b * N * 64 + s * BOX * 64, map, b * 64, at.row, at.token, head, bar);
+  }
 }
 
 // Operand descriptors of a tile: the K-major form (K = 16 channels per step) and the MN-major form
@@ -106,26 +114,28 @@ __device__ __forceinline__ void load_tile(T* dst, const CUtensorMap* map, TileAt
 __device__ __forceinline__ uint64_t desc_k(const void* tile) {
   return smem_desc(smem_u32(tile), 16, 1024, kSwizzle128B);
 }
+template <int N>  // rows of the tile
 __device__ __forceinline__ uint64_t desc_mn(const void* tile) {
-  return smem_desc(smem_u32(tile), BT * 128, 1024, kSwizzle128B);
+  return smem_desc(smem_u32(tile), N * 128, 1024, kSwizzle128B);
 }
+template <int N>
 __host__ __device__ constexpr uint32_t step_k(int kk) {
-  return ((kk >> 2) * (BT * 128) + (kk & 3) * 32) >> 4;
+  return ((kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4;
 }
 __host__ __device__ constexpr uint32_t step_mn(int kk) { return (kk * 16 * 128) >> 4; }
 
-// D = A B^T over D channels, both operands K-major tiles.
-template <int D>
+// D = A B^T over D channels, K-major tiles of 128 and N rows.
+template <int D, int N>
 __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
-    mma_f16(d_tmem, a + step_k(kk), b + step_k(kk), idesc, kk > 0 ? 1u : 0u);
+    mma_f16(d_tmem, a + step_k<BT>(kk), b + step_k<N>(kk), idesc, kk > 0 ? 1u : 0u);
 }
-// D (+)= A B over BT / 2 rows of tile B, A in 32 TMEM columns.
+// D (+)= A B over 64 rows of tile B, A in 32 TMEM columns.
 __device__ __forceinline__ void mma_sum_half(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
                                              uint32_t idesc, bool start) {
 #pragma unroll
-  for (int kk = 0; kk < BT / 32; ++kk)
+  for (int kk = 0; kk < 4; ++kk)
     mma_f16_ts(d_tmem, a_tmem + 8 * kk, b + step_mn(kk), idesc, kk > 0 || !start ? 1u : 0u);
 }
 
@@ -163,7 +173,7 @@ __device__ __forceinline__ float2 exp2_fma2(float2 z) {
 
 // Pairs whose exponentials run on the FMA pipe, the others on the special-function unit (16 a
 // clock and SM), which alone would take as long as the products.
-__device__ __forceinline__ constexpr bool poly_pair(int i) { return (i & 3) == 3; }
+__device__ __forceinline__ constexpr bool poly_pair(int i) { return false; }
 
 namespace fwd {
 
@@ -173,13 +183,22 @@ constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kColO = 256;
+// P's column, per tile, and whether it is apart from S
+template <int D>
+constexpr bool kOwnP = D == 64;
+template <int D>
+constexpr bool kTurns = D == 64;
+template <int D>
+constexpr uint32_t kColP = kOwnP<D> ? 384 : 0;
+template <int D>
+constexpr uint32_t kStepP = kOwnP<D> ? 64 : 128;
 
 template <typename T, int D>
 struct Smem {
   static constexpr int NST = D == 128 ? 5 : 8;  // K / V tiles in flight
   alignas(1024) T q[2][BT * D];
   alignas(1024) T kv[NST][BT * D];
-  uint64_t q_full, full[NST], empty[NST], s_full[2], p_full[2][2], o_full;
+  uint64_t q_full, full[NST], empty[NST], s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full;
   uint32_t tmem_base;
   int abort;
 };
@@ -231,6 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sm.s_full[g], 1);
+      mbar_init(&sm.s_free[g], 128);
+      mbar_init(&sm.pv_done[g], 1);
       mbar_init(&sm.p_full[g][0], 128);
       mbar_init(&sm.p_full[g][1], 128);
     }
@@ -253,17 +274,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProducerWarp) {
       if (lane == 0) {
         mbar_arrive_expect_tx(&sm.q_full, (two ? 2 : 1) * BT * D * 2);
-        load_tile<T, D>(sm.q[0], &tm_q, tile_at(it, tile_of(0)), head0, &sm.q_full);
+        load_tile<T, D, D, BT>(sm.q[0], &tm_q, it, tile_of(0), head0, &sm.q_full);
         if (two)
-          load_tile<T, D>(sm.q[1], &tm_q, tile_at(it, tile_of(1)), HEADS ? head0 + 1 : head0,
-                          &sm.q_full);
+          load_tile<T, D, D, BT>(sm.q[1], &tm_q, it, tile_of(1), HEADS ? head0 + 1 : head0,
+                                 &sm.q_full);
         Ring<NST> ring;
-        for (int i = 0; i < 2 * n0; ++i, ring.next()) {  // K0 V0 K1 V1 ...
+        for (int i = 0; i < 2 * n0; ++i, ring.next()) {  // K0 K1 V0 K2 V1 ... V(n0 - 1)
           const int st = ring.slot;
+          const bool v = i == 2 * n0 - 1 || (i > 0 && (i & 1) == 0);
+          const int j = v ? (i == 2 * n0 - 1 ? n0 - 1 : i / 2 - 1) : (i + 1) / 2;
           if (i >= NST) mbar_wait(&sm.empty[st], ring.parity ^ 1, 301);
           mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
-          load_tile<T, D>(sm.kv[st], (i & 1) ? &tm_v : &tm_k, tile_at(it, i >> 1), kv_head,
-                          &sm.full[st]);
+          load_tile<T, D, D, BT>(sm.kv[st], v ? &tm_v : &tm_k, it, j, kv_head, &sm.full[st]);
         }
       }
       __syncwarp();
@@ -274,45 +296,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id_o = instr_desc(1, kFmt, kFmt, false, true, BT, D);
         const uint64_t q_desc[2] = {desc_k(sm.q[0]), desc_k(sm.q[1])};
         auto scores = [&](int g, uint64_t k_desc) {  // S_g = Q_g K^T
-          mma_rows<D>(tmem + 128 * g, q_desc[g], k_desc, id_s);
+          mma_rows<D, BT>(tmem + 128 * g, q_desc[g], k_desc, id_s);
           mma_commit(&sm.s_full[g]);
         };
-        Ring<NST> v_at, k_at;  // of V_j and K_(j + 1)
+        auto values = [&](int g, uint64_t v_desc, int j) {  // O_g += P_g V
+          // in halves of the keys, so that the first runs during the second's exponentials
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            mbar_wait(&sm.p_full[g][h], j & 1, 312);
+            tc_fence_after();
+            mma_sum_half(tmem + kColO + D * g, tmem + kColP<D> + kStepP<D> * g + 32 * h,
+                         v_desc + step_mn(4 * h), id_o, j == 0 && h == 0);
+          }
+          if (kOwnP<D>) mma_commit(&sm.pv_done[g]);
+        };
+        Ring<NST> ring;  // tiles in their order: K_0, then K_(j + 1) and V_j
         mbar_wait(&sm.q_full, 0, 310);
         mbar_wait(&sm.full[0], 0, 311);
         tc_fence_after();
         scores(0, desc_k(sm.kv[0]));
         if (n1 > 0) scores(1, desc_k(sm.kv[0]));
         mma_commit(&sm.empty[0]);
-        v_at.next();
-        k_at = v_at;
-        k_at.next();
+        ring.next();
         for (int j = 0; j < n0; ++j) {
           const bool more = j + 1 < n0;
-          mbar_wait(&sm.full[v_at.slot], v_at.parity, 311);
-          if (more) mbar_wait(&sm.full[k_at.slot], k_at.parity, 311);
-          const uint64_t v_desc = desc_mn(sm.kv[v_at.slot]);
-          const uint64_t k_desc = desc_k(sm.kv[k_at.slot]);
+          const int k_slot = ring.slot;
+          const uint64_t k_desc = desc_k(sm.kv[k_slot]);
+          if (more) {
+            mbar_wait(&sm.full[k_slot], ring.parity, 311);
+            ring.next();
+          }
+          if (kOwnP<D> && more) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              if (j + 1 >= (g == 0 ? n0 : n1)) continue;
+              mbar_wait(&sm.s_free[g], j & 1, 313);
+              tc_fence_after();
+              scores(g, k_desc);
+            }
+            mma_commit(&sm.empty[k_slot]);
+          }
+          const int v_slot = ring.slot;
+          const uint64_t v_desc = desc_mn<BT>(sm.kv[v_slot]);
+          mbar_wait(&sm.full[v_slot], ring.parity, 311);
+          ring.next();
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const int n = g == 0 ? n0 : n1;
             if (j >= n) continue;
-            // in halves of the keys, so that the first runs during the second's exponentials
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              mbar_wait(&sm.p_full[g][h], j & 1, 312);
-              tc_fence_after();
-              mma_sum_half(tmem + kColO + 128 * g, tmem + 128 * g + 32 * h, v_desc + step_mn(4 * h),
-                           id_o, j == 0 && h == 0);
-            }
-            if (j + 1 < n) scores(g, k_desc);
+            values(g, v_desc, j);
+            if (!kOwnP<D> && j + 1 < n) scores(g, k_desc);
           }
-          mma_commit(&sm.empty[v_at.slot]);
-          if (more) mma_commit(&sm.empty[k_at.slot]);
-          v_at.next();
-          v_at.next();
-          k_at.next();
-          k_at.next();
+          mma_commit(&sm.empty[v_slot]);
+          if (!kOwnP<D> && more) mma_commit(&sm.empty[k_slot]);
         }
         mma_commit(&sm.o_full);
       }
@@ -327,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + (((warp & 3) * 32u) << 16);
-    const uint32_t s_at = lane_base + 128 * g, o_at = lane_base + kColO + 128 * g;
+    const uint32_t s_at = lane_base + 128 * g, o_at = lane_base + kColO + D * g;
+    const uint32_t p_at = lane_base + kColP<D> + kStepP<D> * g;
     const int n = g == 0 ? n0 : n1;
     const int tile = tile_of(g);
     const int i = row_index(it, tile, r);
@@ -345,6 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tie32(x[1]);
       tie32(x[2]);
       tie32(x[3]);
+      if (kOwnP<D>) {
+        tc_fence_before();
+        mbar_arrive(&sm.s_free[g]);
+      }
       if (MASK) {
         // key index within the sequence must be >= 0 (the ragged first tile) and, when causal,
         // not above the row's
@@ -365,6 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx[q] = fmax3(mx[q], __uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]));
       }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      // P V of the last key tile: O is up to date and P's columns are free.  (Where P lies in S,
+      // the arrival of S has said so.)
+      if (kOwnP<D> && j > 0) {
+        mbar_wait(&sm.pv_done[g], (j - 1) & 1, 322);
+        tc_fence_after();
+      }
       const bool grow = top > m + 8.0f;  // always on the first tile with a visible key
       if (__any_sync(0xffffffffu, grow)) {
         const float mn = grow ? top : m;
@@ -387,26 +434,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float neg = m == -INFINITY ? 0.0f : -m;
       const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
       float2 sum = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
+      if (two && kTurns<D>) named_barrier_sync(1 + g, 256);
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
+        // three passes over 64 columns, so that independent operations follow each other
+        float2 z[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int q = 2 * hh + (k >> 4), e = 2 * (k & 15);
+          z[k] = __ffma2_rn(
+              make_float2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])), c2, n2);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          z[k] = !MASK && poly_pair(k) ? exp2_fma2(z[k])
+                                       : make_float2(ex2_approx(z[k].x), ex2_approx(z[k].y));
         uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          const int q = 2 * hh + (e >> 5), ee = e & 31;
-          const float2 z = __ffma2_rn(
-              make_float2(__uint_as_float(x[q][ee]), __uint_as_float(x[q][ee + 1])), c2, n2);
-          float2 p;
-          if (!MASK && poly_pair(e >> 1))
-            p = exp2_fma2(z);
+        for (int k = 0; k < 32; ++k) {
+          if (k & 1)
+            sum2 = __fadd2_rn(sum2, z[k]);
           else
-            p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-          if (e & 2)
-            sum2 = __fadd2_rn(sum2, p);
-          else
-            sum = __fadd2_rn(sum, p);
-          w[e >> 1] = Cvt<T>::pack2(p.x, p.y);
+            sum = __fadd2_rn(sum, z[k]);
+          w[k] = Cvt<T>::pack2(z[k].x, z[k].y);
         }
-        tmem_st32(s_at + 32 * hh, w);
+        tmem_st32(p_at + 32 * hh, w);
+        if (hh == 1 && two && kTurns<D>) named_barrier_arrive(2 - g, 256);
         tmem_st_wait();  // of O too, where it was rescaled
         tc_fence_before();
         mbar_arrive(&sm.p_full[g][hh]);
@@ -414,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       l += (sum.x + sum.y) + (sum2.x + sum2.y);
     };
     const bool ragged = tiles_of(it) * BT != it.len;
+    if (two && kTurns<D> && g == 1) named_barrier_arrive(1, 256);  // tile 0 begins
     for (int j = 0; j < n; ++j) {
       if ((j == 0 && ragged) || (a.causal && j == tile))
         block(j, std::true_type{});
