@@ -293,21 +293,29 @@ int run_packed_fwd(const sage_packed_params* p, const sage_packed_info* info, co
     return SAGE_ERR_CUDA;
   F::Args a;
   a.group = p->Hq / p->Hkv;
-  const bool heads = a.group % 2 == 0;
   a.o = packed_out(o);
   a.lse = lse;
   a.T = p->T;
-  const int ctas = heads ? p->Hq / 2 : p->Hq;  // per item
-  const int64_t kv_bytes = info->tokens * D * 2 * 2;
-  a.grid = {plan_list(plan, info, p->causal, !heads), heads ? info->tiles : info->pairs, ctas,
-            grid_chunk(p, info, ctas, kv_bytes / (heads ? a.group / 2 : a.group))};
   a.causal = p->causal;
   a.scale_log2 = packed_tau(p) * 1.4426950408889634f;
-  const int64_t grid = static_cast<int64_t>(a.grid.n_items) * ctas;
-  return heads ? launch_packed(F::attn_fwd_kernel<T, D, true>, F::kLaunchRegs, grid, F::kThreads,
-                               F::smem_bytes<T, D>(), st, tq, tk, tv, a)
-               : launch_packed(F::attn_fwd_kernel<T, D, false>, F::kLaunchRegs, grid, F::kThreads,
-                               F::smem_bytes<T, D>(), st, tq, tk, tv, a);
+  const int64_t kv_bytes = info->tokens * D * 2 * 2;
+  if constexpr (D == 64) {
+    a.grid = {plan_list(plan, info, p->causal, false), info->tiles, p->Hq,
+              grid_chunk(p, info, p->Hq, kv_bytes / a.group)};
+    return launch_packed(F::attn_fwd64_kernel<T>, F::kLaunchRegs64,
+                         static_cast<int64_t>(info->tiles) * p->Hq, F::kThreads64,
+                         F::smem64_bytes<T>(), st, tq, tk, tv, a);
+  } else {
+    const bool heads = a.group % 2 == 0;
+    const int ctas = heads ? p->Hq / 2 : p->Hq;  // per item
+    a.grid = {plan_list(plan, info, p->causal, !heads), heads ? info->tiles : info->pairs, ctas,
+              grid_chunk(p, info, ctas, kv_bytes / (heads ? a.group / 2 : a.group))};
+    const int64_t grid = static_cast<int64_t>(a.grid.n_items) * ctas;
+    return heads ? launch_packed(F::attn_fwd_kernel<T, D, true>, F::kLaunchRegs, grid, F::kThreads,
+                                 F::smem_bytes<T, D>(), st, tq, tk, tv, a)
+                 : launch_packed(F::attn_fwd_kernel<T, D, false>, F::kLaunchRegs, grid,
+                                 F::kThreads, F::smem_bytes<T, D>(), st, tq, tk, tv, a);
+  }
 }
 
 // Workspace: D [Hq][T]; in half precision also the norms [sequences][Hkv][2].

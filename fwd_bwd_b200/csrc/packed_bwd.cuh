@@ -483,7 +483,7 @@ struct DqSmem {
   alignas(1024) T dout[BT * D];
   alignas(1024) T ring[NST][BN * D];
   float dot[2][BT];  // halves of D, where the row pass's is replaced
-  uint64_t q_full, full[NST], empty[NST], s_full[2], dp_full, dp_free, ds_ready, done;
+  uint64_t q_full, full[NST], empty[NST], s_full[2], dp_full, dp_free, ds_ready[2], done;
   uint32_t tmem_base;
   int abort;
 };
@@ -530,7 +530,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     mbar_init(&sm.s_full[1], 1);
     mbar_init(&sm.dp_full, 1);
     mbar_init(&sm.dp_free, C::kCompute);
-    mbar_init(&sm.ds_ready, C::kCompute);
+    // two, because dP of the next run is issued before this one's dS is waited for
+    mbar_init(&sm.ds_ready[0], C::kCompute);
+    mbar_init(&sm.ds_ready[1], C::kCompute);
     mbar_init(&sm.done, 1);
     fence_barrier_init();
   }
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
             v_at.next();
             v_at.next();
           }
-          mbar_wait(&sm.ds_ready, n & 1, 513);
+          mbar_wait(&sm.ds_ready[n & 1], (n >> 1) & 1, 513);
           tc_fence_after();
           // dQ += dS K
           if (n >= pre)
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
         }
         tc_fence_before();
         mbar_arrive(&sm.dp_free);
-        mbar_arrive(&sm.ds_ready);
+        mbar_arrive(&sm.ds_ready[n & 1]);
         dvec += (sum.x + sum.y) * exp2f(-Scaling<T>::kPShift);
         if (n == pre - 1) {
           if (C::kWG == 2) {
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sm.ds_ready);
+      mbar_arrive(&sm.ds_ready[n & 1]);
     };
     for (int n = 0; n < n_all; ++n) {
       const int run = run_of(n);

@@ -10,22 +10,30 @@
 // the TMA unit reads as zeros, so no row of a neighbouring sequence ever enters shared memory
 // and non-finite values cannot leak through a product with a zero probability.
 //
-// Per CTA: two query tiles that share their keys: two heads of one group (an even number of
-// query heads per key head), else two neighbouring tiles of one head.
+// attn_fwd_kernel (d = 128), per CTA: two query tiles that share their keys: two heads of one group
+// (an even number of query heads per key head), else two neighbouring tiles of one head.
 //   warps 0-3, 4-7  softmax of tile 0 / 1, one query row per thread
 //   warp 8          TMA producer: the query tiles, then K and V tiles through a ring
 //   warp 9          MMA issuer: S = Q K^T (operands in shared memory), O += P V (P in TMEM)
 //   warps 10-11     idle (they complete the warpgroup that gives its registers away)
-// TMEM: S of tile g at 128 g, O of tile g at 256 + D g, accumulated there over all keys.
-//   d = 128 fills TMEM: P (two 16-bit values to a column) overwrites the first half of its S, so S
-//   of the next key tile is issued after P V of this one; the tensor core alternates between the
-//   tiles: while tile 0's softmax runs, it multiplies tile 1's P V and Q K^T.
-//   d = 64 leaves room for P of its own (at 384 + 64 g): S of the next key tile is issued as soon
-//   as this one has been read, and waits for the softmax warps instead of the reverse.
-// The running maximum that P is taken against is raised (and O rescaled in TMEM) only when a
-// row's maximum grows by more than 2^8: P then stays below 256, exact in the final division
+// TMEM: S of tile g at 128 g (P overwrites its first 64 columns, two 16-bit values each), O of
+// tile g at 256 + 128 g, accumulated there over all keys.
+// The tensor core alternates between the tiles: while tile 0's softmax runs, it multiplies tile
+// 1's P V and Q K^T.  S of the next key tile is issued after P V of this one, so its arrival
+// also tells the softmax warps that O is up to date.
+//
+// attn_fwd64_kernel (d = 64), per CTA: one query tile, keys in runs of 64, half an SM's TMEM,
+// registers and shared memory, so that two CTAs share an SM and hide each other's latencies, first
+// loads and last stores included (they take a quarter of a CTA's time at 2048 tokens).  S and P
+// have two buffers each: S of the next run is ready before this one's softmax ends.
+//
+// Both: the running maximum that P is taken against is raised (and O rescaled in TMEM) only when
+// a row's maximum grows by more than 2^8: P then stays below 256, exact in the final division
 // by the row sum, and most key tiles leave O untouched.
 // Rounding: P to the tensors' type for P V (the sum l uses the unrounded P); O once at the end.
+// The exponentials all go to the special-function unit: moving an eighth or a quarter of them to
+// the FMA pipe costs more instructions than it frees time (16 heads of 128, 4 x 8192 tokens:
+// 899 us, 921 us and 953 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -171,10 +179,6 @@ __device__ __forceinline__ float2 exp2_fma2(float2 z) {
                      __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
 }
 
-// Pairs whose exponentials run on the FMA pipe, the others on the special-function unit (16 a
-// clock and SM), which alone would take as long as the products.
-__device__ __forceinline__ constexpr bool poly_pair(int i) { return false; }
-
 namespace fwd {
 
 constexpr int kThreads = 384;
@@ -183,22 +187,13 @@ constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr uint32_t kColO = 256;
-// P's column, per tile, and whether it is apart from S
-template <int D>
-constexpr bool kOwnP = D == 64;
-template <int D>
-constexpr bool kTurns = D == 64;
-template <int D>
-constexpr uint32_t kColP = kOwnP<D> ? 384 : 0;
-template <int D>
-constexpr uint32_t kStepP = kOwnP<D> ? 64 : 128;
-
 template <typename T, int D>
 struct Smem {
-  static constexpr int NST = D == 128 ? 5 : 8;  // K / V tiles in flight
+  static_assert(D == 128, "two tiles of d = 128 fill TMEM; d = 64 has its own kernel");
+  static constexpr int NST = 5;  // K / V tiles in flight
   alignas(1024) T q[2][BT * D];
   alignas(1024) T kv[NST][BT * D];
-  uint64_t q_full, full[NST], empty[NST], s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full;
+  uint64_t q_full, full[NST], empty[NST], s_full[2], p_full[2][2], o_full;
   uint32_t tmem_base;
   int abort;
 };
@@ -250,8 +245,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sm.s_full[g], 1);
-      mbar_init(&sm.s_free[g], 128);
-      mbar_init(&sm.pv_done[g], 1);
       mbar_init(&sm.p_full[g][0], 128);
       mbar_init(&sm.p_full[g][1], 128);
     }
@@ -305,10 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2; ++h) {
             mbar_wait(&sm.p_full[g][h], j & 1, 312);
             tc_fence_after();
-            mma_sum_half(tmem + kColO + D * g, tmem + kColP<D> + kStepP<D> * g + 32 * h,
-                         v_desc + step_mn(4 * h), id_o, j == 0 && h == 0);
+            mma_sum_half(tmem + kColO + D * g, tmem + 128 * g + 32 * h, v_desc + step_mn(4 * h),
+                         id_o, j == 0 && h == 0);
           }
-          if (kOwnP<D>) mma_commit(&sm.pv_done[g]);
         };
         Ring<NST> ring;  // tiles in their order: K_0, then K_(j + 1) and V_j
         mbar_wait(&sm.q_full, 0, 310);
@@ -326,16 +318,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(&sm.full[k_slot], ring.parity, 311);
             ring.next();
           }
-          if (kOwnP<D> && more) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              if (j + 1 >= (g == 0 ? n0 : n1)) continue;
-              mbar_wait(&sm.s_free[g], j & 1, 313);
-              tc_fence_after();
-              scores(g, k_desc);
-            }
-            mma_commit(&sm.empty[k_slot]);
-          }
           const int v_slot = ring.slot;
           const uint64_t v_desc = desc_mn<BT>(sm.kv[v_slot]);
           mbar_wait(&sm.full[v_slot], ring.parity, 311);
@@ -345,10 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = g == 0 ? n0 : n1;
             if (j >= n) continue;
             values(g, v_desc, j);
-            if (!kOwnP<D> && j + 1 < n) scores(g, k_desc);
+            if (j + 1 < n) scores(g, k_desc);
           }
           mma_commit(&sm.empty[v_slot]);
-          if (!kOwnP<D> && more) mma_commit(&sm.empty[k_slot]);
+          if (more) mma_commit(&sm.empty[k_slot]);
         }
         mma_commit(&sm.o_full);
       }
@@ -364,7 +346,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + (((warp & 3) * 32u) << 16);
     const uint32_t s_at = lane_base + 128 * g, o_at = lane_base + kColO + D * g;
-    const uint32_t p_at = lane_base + kColP<D> + kStepP<D> * g;
     const int n = g == 0 ? n0 : n1;
     const int tile = tile_of(g);
     const int i = row_index(it, tile, r);
@@ -382,10 +363,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tie32(x[1]);
       tie32(x[2]);
       tie32(x[3]);
-      if (kOwnP<D>) {
-        tc_fence_before();
-        mbar_arrive(&sm.s_free[g]);
-      }
       if (MASK) {
         // key index within the sequence must be >= 0 (the ragged first tile) and, when causal,
         // not above the row's
@@ -406,12 +383,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx[q] = fmax3(mx[q], __uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]));
       }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      // P V of the last key tile: O is up to date and P's columns are free.  (Where P lies in S,
-      // the arrival of S has said so.)
-      if (kOwnP<D> && j > 0) {
-        mbar_wait(&sm.pv_done[g], (j - 1) & 1, 322);
-        tc_fence_after();
-      }
       const bool grow = top > m + 8.0f;  // always on the first tile with a visible key
       if (__any_sync(0xffffffffu, grow)) {
         const float mn = grow ? top : m;
@@ -434,7 +405,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float neg = m == -INFINITY ? 0.0f : -m;
       const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
       float2 sum = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
-      if (two && kTurns<D>) named_barrier_sync(1 + g, 256);
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         // three passes over 64 columns, so that independent operations follow each other
@@ -447,8 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          z[k] = !MASK && poly_pair(k) ? exp2_fma2(z[k])
-                                       : make_float2(ex2_approx(z[k].x), ex2_approx(z[k].y));
+          z[k] = make_float2(ex2_approx(z[k].x), ex2_approx(z[k].y));
         uint32_t w[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
@@ -458,8 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum = __fadd2_rn(sum, z[k]);
           w[k] = Cvt<T>::pack2(z[k].x, z[k].y);
         }
-        tmem_st32(p_at + 32 * hh, w);
-        if (hh == 1 && two && kTurns<D>) named_barrier_arrive(2 - g, 256);
+        tmem_st32(s_at + 32 * hh, w);
         tmem_st_wait();  // of O too, where it was rescaled
         tc_fence_before();
         mbar_arrive(&sm.p_full[g][hh]);
@@ -467,7 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       l += (sum.x + sum.y) + (sum2.x + sum2.y);
     };
     const bool ragged = tiles_of(it) * BT != it.len;
-    if (two && kTurns<D> && g == 1) named_barrier_arrive(1, 256);  // tile 0 begins
     for (int j = 0; j < n; ++j) {
       if ((j == 0 && ragged) || (a.causal && j == tile))
         block(j, std::true_type{});
@@ -500,6 +467,247 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     named_barrier_sync(15, kThreads);
+  }
+}
+
+// ---- d = 64 ---------------------------------------------------------------------------------
+constexpr int kThreads64 = 256;
+constexpr int kProducerWarp64 = 4, kMmaWarp64 = 5;
+constexpr int kLaunchRegs64 = 128, kSoftmaxRegs64 = 184, kOtherRegs64 = 72;
+static_assert(128 * (kSoftmaxRegs64 + kOtherRegs64) <= kThreads64 * kLaunchRegs64,
+              "register split exceeds the launch allocation");
+
+template <typename T>
+struct Smem64 {
+  static constexpr int NST = 8;  // K / V runs in flight
+  alignas(1024) T q[BT * 64];
+  alignas(1024) T kv[NST][64 * 64];
+  uint64_t q_full, full[NST], empty[NST], s_full[2], p_full[2], pv_done, o_full;
+  uint32_t tmem_base;
+  int abort;
+};
+template <typename T>
+constexpr size_t smem64_bytes() {
+  return sizeof(Smem64<T>) + 1024;
+}
+static_assert(smem64_bytes<__half>() <= 115712, "shared memory of two CTAs exceeds the limit");
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads64, 2)
+    attn_fwd64_kernel(const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const Args a) {
+  constexpr int D = 64, BN = 64;
+  extern __shared__ uint8_t smem_raw[];
+  using SM = Smem64<T>;
+  SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  constexpr int NST = SM::NST;
+  // TMEM columns: S of even and odd runs at 0 and 64, O, P of even and odd runs
+  constexpr uint32_t kColO64 = 128, kColP64 = 192;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int head;
+  const Item it = grid_at(a.grid, head);
+  const int kv_head = head / a.group;
+  const int tiles = tiles_of(it), pad = tiles * BT - it.len;
+  const int first = pad / BN;  // a run that is all padding is left out
+  const int n = (a.causal ? it.tile + 1 : tiles) * (BT / BN) - first;
+
+  if (threadIdx.x == 0) {
+    sm.abort = device_aborted() ? 1 : 0;
+    mbar_init(&sm.q_full, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    mbar_init(&sm.s_full[0], 1);
+    mbar_init(&sm.s_full[1], 1);
+    mbar_init(&sm.p_full[0], 128);
+    mbar_init(&sm.p_full[1], 128);
+    mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.o_full, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (sm.abort) return;
+  if (warp == kMmaWarp64) {
+    tmem_alloc(&sm.tmem_base, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs64));
+    if (warp == kProducerWarp64) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sm.q_full, BT * D * 2);
+        load_tile<T, D, BN, BT>(sm.q, &tm_q, it, it.tile, head, &sm.q_full);
+        Ring<NST> ring;
+        for (int i = 0; i < 2 * n; ++i, ring.next()) {  // K0 K1 V0 K2 V1 ... V(n - 1)
+          const int st = ring.slot;
+          const bool v = i == 2 * n - 1 || (i > 0 && (i & 1) == 0);
+          const int j = v ? (i == 2 * n - 1 ? n - 1 : i / 2 - 1) : (i + 1) / 2;
+          if (i >= NST) mbar_wait(&sm.empty[st], ring.parity ^ 1, 331);
+          mbar_arrive_expect_tx(&sm.full[st], BN * D * 2);
+          load_tile<T, D, BN, BN>(sm.kv[st], v ? &tm_v : &tm_k, it, first + j, kv_head,
+                                  &sm.full[st]);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp64) {
+      if (lane == 0) {
+        constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+        constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
+        constexpr uint32_t id_o = instr_desc(1, kFmt, kFmt, false, true, BT, D);
+        const uint64_t q_desc = desc_k(sm.q);
+        Ring<NST> ring;
+        auto scores = [&](int b) {  // S of the next K run
+          mbar_wait(&sm.full[ring.slot], ring.parity, 341);
+          tc_fence_after();
+          mma_rows<D, BN>(tmem + BN * b, q_desc, desc_k(sm.kv[ring.slot]), id_s);
+          mma_commit(&sm.s_full[b]);
+          mma_commit(&sm.empty[ring.slot]);
+          ring.next();
+        };
+        mbar_wait(&sm.q_full, 0, 340);
+        scores(0);
+        if (n > 1) scores(1);
+        for (int j = 0; j < n; ++j) {
+          mbar_wait(&sm.full[ring.slot], ring.parity, 342);
+          mbar_wait(&sm.p_full[j & 1], (j >> 1) & 1, 343);
+          tc_fence_after();
+          // O += P V
+          mma_sum_half(tmem + kColO64, tmem + kColP64 + 32 * (j & 1),
+                       desc_mn<BN>(sm.kv[ring.slot]), id_o, j == 0);
+          mma_commit(&sm.pv_done);
+          mma_commit(&sm.empty[ring.slot]);
+          ring.next();
+          // its arrival also says that P V of run j is done: P's buffer is free for run j + 2
+          if (j + 2 < n) scores(j & 1);
+        }
+        mma_commit(&sm.o_full);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    named_barrier_sync(15, kThreads64);
+    tc_fence_after();
+    if (warp == kMmaWarp64) tmem_dealloc(tmem, 256);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs64));
+    const int r = threadIdx.x;
+    const uint32_t lane_base = tmem + ((warp * 32u) << 16);
+    const uint32_t o_at = lane_base + kColO64;
+    const int i = row_index(it, it.tile, r);
+    const float c = a.scale_log2;
+    float m = -INFINITY, l = 0.0f;
+
+    auto block = [&](int j, auto masked) {
+      constexpr bool MASK = decltype(masked)::value;
+      const uint32_t s_at = lane_base + BN * (j & 1), p_at = lane_base + kColP64 + 32 * (j & 1);
+      mbar_wait(&sm.s_full[j & 1], (j >> 1) & 1, 350);
+      tc_fence_after();
+      uint32_t x[2][32];
+      tmem_ld32(s_at, x[0]);
+      tmem_ld32(s_at + 32, x[1]);
+      tmem_ld_wait_regs32(x[0]);
+      tie32(x[1]);
+      if (MASK) {
+        // key index within the sequence >= 0 (ragged first run) and, when causal, not above i
+        const int key0 = row_index<BN>(it, first + j, 0);
+        const int lo = -key0, hi = a.causal ? i - key0 : BN;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * q + e < lo || 32 * q + e > hi) x[q][e] = 0xff800000u;  // -inf
+      }
+      float mx[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t* y = &x[q >> 1][16 * (q & 1)];
+        mx[q] = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+#pragma unroll
+        for (int e = 2; e < 16; e += 2)
+          mx[q] = fmax3(mx[q], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      const bool grow = top > m + 8.0f;  // always on the first run with a visible key
+      if (__any_sync(0xffffffffu, grow)) {
+        const float mn = grow ? top : m;
+        const float alpha = grow ? ex2_approx(m - mn) : 1.0f;
+        m = mn;
+        l *= alpha;
+        if (j > 0) {
+          mbar_wait(&sm.pv_done, (j - 1) & 1, 351);  // O is up to date
+          tc_fence_after();
+#pragma unroll
+          for (int cc = 0; cc < D; cc += 16) {
+            uint32_t y[16];
+            tmem_ld16(o_at + cc, y);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              asm volatile("" : "+r"(y[e]));
+              y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+            }
+            tmem_st16(o_at + cc, y);
+          }
+        }
+      }
+      const float neg = m == -INFINITY ? 0.0f : -m;
+      const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
+      float2 sum = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
+      uint32_t w[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const int q = k >> 4, e = 2 * (k & 15);
+        const float2 z = __ffma2_rn(
+            make_float2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])), c2, n2);
+        const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+        if (k & 1)
+          sum2 = __fadd2_rn(sum2, p);
+        else
+          sum = __fadd2_rn(sum, p);
+        w[k] = Cvt<T>::pack2(p.x, p.y);
+      }
+      tmem_st32(p_at, w);
+      tmem_st_wait();  // of O too, where it was rescaled
+      tc_fence_before();
+      mbar_arrive(&sm.p_full[j & 1]);
+      l += (sum.x + sum.y) + (sum2.x + sum2.y);
+    };
+    for (int j = 0; j < n; ++j) {
+      if ((j == 0 && pad > 0) || (a.causal && first + j >= it.tile * (BT / BN)))
+        block(j, std::true_type{});
+      else
+        block(j, std::false_type{});
+    }
+    mbar_wait(&sm.o_full, 0, 352);
+    tc_fence_after();
+    const float inv_l = 1.0f / l;
+    const int64_t row = static_cast<int64_t>(it.start) + i;
+    T* out = reinterpret_cast<T*>(a.o.ptr) + row * a.o.ts + head * a.o.hs;
+#pragma unroll
+    for (int cc = 0; cc < D; cc += 32) {
+      uint32_t y[32];
+      tmem_ld32(o_at + cc, y);
+      tmem_ld_wait_regs32(y);
+      if (i >= 0) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * inv_l;
+          *reinterpret_cast<uint4*>(out + cc + e) = pack8<T>(f);
+        }
+      }
+    }
+    if (i >= 0) a.lse[head * a.T + row] = (m + log2f(l)) * 0.69314718055994531f;
+    tc_fence_before();
+    named_barrier_sync(15, kThreads64);
   }
 }
 
