@@ -259,9 +259,9 @@ template <typename K, typename... A>
 int launch_packed(K kern, int regs, int64_t grid, int threads, size_t smem, cudaStream_t st,
                   const A&... args) {
   if (set_smem(kern, smem) != SAGE_OK) return SAGE_ERR_CUDA;
-  // the kernels move registers between warpgroups (setmaxnreg); the split is sized for exactly
+  // kernels that move registers between warpgroups (setmaxnreg): the split is sized for exactly
   // this launch allocation
-  if (launch_regs(kern) != regs) return SAGE_ERR_UNSUPPORTED;
+  if (regs != 0 && launch_regs(kern) != regs) return SAGE_ERR_UNSUPPORTED;
   kern<<<static_cast<unsigned>(grid), threads, smem, st>>>(args...);
   return launch_status();
 }
@@ -302,7 +302,7 @@ int run_packed_fwd(const sage_packed_params* p, const sage_packed_info* info, co
   if constexpr (D == 64) {
     a.grid = {plan_list(plan, info, p->causal, false), info->tiles, p->Hq,
               grid_chunk(p, info, p->Hq, kv_bytes / a.group)};
-    return launch_packed(F::attn_fwd64_kernel<T>, F::kLaunchRegs64,
+    return launch_packed(F::attn_fwd64_kernel<T>, 0,
                          static_cast<int64_t>(info->tiles) * p->Hq, F::kThreads64,
                          F::smem64_bytes<T>(), st, tq, tk, tv, a);
   } else {

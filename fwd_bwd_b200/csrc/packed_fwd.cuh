@@ -22,10 +22,13 @@
 // 1's P V and Q K^T.  S of the next key tile is issued after P V of this one, so its arrival
 // also tells the softmax warps that O is up to date.
 //
-// attn_fwd64_kernel (d = 64), per CTA: one query tile, keys in runs of 64, half an SM's TMEM,
-// registers and shared memory, so that two CTAs share an SM and hide each other's latencies, first
-// loads and last stores included (they take a quarter of a CTA's time at 2048 tokens).  S and P
-// have two buffers each: S of the next run is ready before this one's softmax ends.
+// attn_fwd64_kernel (d = 64), per CTA: one query tile, keys in runs of 64, a quarter of an SM's TMEM,
+// registers and shared memory: the products of d = 64 are short and the softmax is a chain of
+// latencies, so four CTAs share an SM and hide each other's, first loads and last stores included.
+//   warps 0-3  softmax, one query row per thread;  warp 4  TMA and MMA issue
+// TMEM: S at 0 (P over its first 32 columns), O at 64.  One thread issues everything: once P of a
+// run has arrived, the run's Q K^T and the last run's P V are complete, so their K and V
+// buffers are free without further barriers.
 //
 // Both: the running maximum that P is taken against is raised (and O rescaled in TMEM) only when
 // a row's maximum grows by more than 2^8: P then stays below 256, exact in the final division
@@ -471,18 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- d = 64 ---------------------------------------------------------------------------------
-constexpr int kThreads64 = 256;
-constexpr int kProducerWarp64 = 4, kMmaWarp64 = 5;
-constexpr int kLaunchRegs64 = 128, kSoftmaxRegs64 = 184, kOtherRegs64 = 72;
-static_assert(128 * (kSoftmaxRegs64 + kOtherRegs64) <= kThreads64 * kLaunchRegs64,
-              "register split exceeds the launch allocation");
+constexpr int kThreads64 = 160;
+constexpr int kIssueWarp64 = 4;
 
 template <typename T>
 struct Smem64 {
-  static constexpr int NST = 8;  // K / V runs in flight
   alignas(1024) T q[BT * 64];
-  alignas(1024) T kv[NST][64 * 64];
-  uint64_t q_full, full[NST], empty[NST], s_full[2], p_full[2], pv_done, o_full;
+  alignas(1024) T k[2][64 * 64], v[2][64 * 64];  // even and odd runs
+  uint64_t q_full, k_full[2], v_full[2], s_full, p_full, o_full;
   uint32_t tmem_base;
   int abort;
 };
@@ -490,10 +489,11 @@ template <typename T>
 constexpr size_t smem64_bytes() {
   return sizeof(Smem64<T>) + 1024;
 }
-static_assert(smem64_bytes<__half>() <= 115712, "shared memory of two CTAs exceeds the limit");
+static_assert(4 * (smem64_bytes<__half>() + 1024) <= 233472,
+              "shared memory of four CTAs exceeds the limit");
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads64, 2)
+__global__ void __launch_bounds__(kThreads64, 4)
     attn_fwd64_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Args a) {
@@ -501,9 +501,7 @@ __global__ void __launch_bounds__(kThreads64, 2)
   extern __shared__ uint8_t smem_raw[];
   using SM = Smem64<T>;
   SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-  constexpr int NST = SM::NST;
-  // TMEM columns: S of even and odd runs at 0 and 64, O, P of even and odd runs
-  constexpr uint32_t kColO64 = 128, kColP64 = 192;
+  constexpr uint32_t kColO64 = 64;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int head;
   const Item it = grid_at(a.grid, head);
@@ -515,22 +513,19 @@ __global__ void __launch_bounds__(kThreads64, 2)
   if (threadIdx.x == 0) {
     sm.abort = device_aborted() ? 1 : 0;
     mbar_init(&sm.q_full, 1);
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.v_full[s], 1);
     }
-    mbar_init(&sm.s_full[0], 1);
-    mbar_init(&sm.s_full[1], 1);
-    mbar_init(&sm.p_full[0], 128);
-    mbar_init(&sm.p_full[1], 128);
-    mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.p_full, 128);
     mbar_init(&sm.o_full, 1);
     fence_barrier_init();
   }
   __syncthreads();
   if (sm.abort) return;
-  if (warp == kMmaWarp64) {
-    tmem_alloc(&sm.tmem_base, 256);
+  if (warp == kIssueWarp64) {
+    tmem_alloc(&sm.tmem_base, 128);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -538,65 +533,54 @@ __global__ void __launch_bounds__(kThreads64, 2)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  if (warp >= 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs64));
-    if (warp == kProducerWarp64) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sm.q_full, BT * D * 2);
-        load_tile<T, D, BN, BT>(sm.q, &tm_q, it, it.tile, head, &sm.q_full);
-        Ring<NST> ring;
-        for (int i = 0; i < 2 * n; ++i, ring.next()) {  // K0 K1 V0 K2 V1 ... V(n - 1)
-          const int st = ring.slot;
-          const bool v = i == 2 * n - 1 || (i > 0 && (i & 1) == 0);
-          const int j = v ? (i == 2 * n - 1 ? n - 1 : i / 2 - 1) : (i + 1) / 2;
-          if (i >= NST) mbar_wait(&sm.empty[st], ring.parity ^ 1, 331);
-          mbar_arrive_expect_tx(&sm.full[st], BN * D * 2);
-          load_tile<T, D, BN, BN>(sm.kv[st], v ? &tm_v : &tm_k, it, first + j, kv_head,
-                                  &sm.full[st]);
+  if (warp == kIssueWarp64) {
+    if (lane == 0) {
+      constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
+      constexpr uint32_t id_o = instr_desc(1, kFmt, kFmt, false, true, BT, D);
+      auto load = [&](T* dst, const CUtensorMap* map, int j, uint64_t* bar) {
+        if (j >= n) return;
+        mbar_arrive_expect_tx(bar, BN * D * 2);
+        load_tile<T, D, BN, BN>(dst, map, it, first + j, kv_head, bar);
+      };
+      mbar_arrive_expect_tx(&sm.q_full, BT * D * 2);
+      load_tile<T, D, BN, BT>(sm.q, &tm_q, it, it.tile, head, &sm.q_full);
+      load(sm.k[0], &tm_k, 0, &sm.k_full[0]);
+      load(sm.v[0], &tm_v, 0, &sm.v_full[0]);
+      load(sm.k[1], &tm_k, 1, &sm.k_full[1]);
+      const uint64_t q_desc = desc_k(sm.q);
+      const uint64_t k_desc[2] = {desc_k(sm.k[0]), desc_k(sm.k[1])};
+      const uint64_t v_desc[2] = {desc_mn<BN>(sm.v[0]), desc_mn<BN>(sm.v[1])};
+      mbar_wait(&sm.q_full, 0, 340);
+      mbar_wait(&sm.k_full[0], 0, 341);
+      tc_fence_after();
+      mma_rows<D, BN>(tmem, q_desc, k_desc[0], id_s);
+      mma_commit(&sm.s_full);
+      for (int j = 0; j < n; ++j) {
+        const int b = j & 1, nb = b ^ 1;
+        const uint32_t parity = (j >> 1) & 1;
+        mbar_wait(&sm.v_full[b], parity, 342);
+        if (j + 1 < n) mbar_wait(&sm.k_full[nb], ((j + 1) >> 1) & 1, 341);
+        mbar_wait(&sm.p_full, j & 1, 343);
+        tc_fence_after();
+        mma_sum_half(tmem + kColO64, tmem, v_desc[b], id_o, j == 0);  // O += P V
+        if (j + 1 < n) {
+          mma_rows<D, BN>(tmem, q_desc, k_desc[nb], id_s);
+          mma_commit(&sm.s_full);
+        } else {
+          mma_commit(&sm.o_full);
         }
+        // P of run j has arrived: S of run j and P V of run j - 1 are complete
+        load(sm.v[nb], &tm_v, j + 1, &sm.v_full[nb]);
+        load(sm.k[b], &tm_k, j + 2, &sm.k_full[b]);
       }
-      __syncwarp();
-    } else if (warp == kMmaWarp64) {
-      if (lane == 0) {
-        constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-        constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
-        constexpr uint32_t id_o = instr_desc(1, kFmt, kFmt, false, true, BT, D);
-        const uint64_t q_desc = desc_k(sm.q);
-        Ring<NST> ring;
-        auto scores = [&](int b) {  // S of the next K run
-          mbar_wait(&sm.full[ring.slot], ring.parity, 341);
-          tc_fence_after();
-          mma_rows<D, BN>(tmem + BN * b, q_desc, desc_k(sm.kv[ring.slot]), id_s);
-          mma_commit(&sm.s_full[b]);
-          mma_commit(&sm.empty[ring.slot]);
-          ring.next();
-        };
-        mbar_wait(&sm.q_full, 0, 340);
-        scores(0);
-        if (n > 1) scores(1);
-        for (int j = 0; j < n; ++j) {
-          mbar_wait(&sm.full[ring.slot], ring.parity, 342);
-          mbar_wait(&sm.p_full[j & 1], (j >> 1) & 1, 343);
-          tc_fence_after();
-          // O += P V
-          mma_sum_half(tmem + kColO64, tmem + kColP64 + 32 * (j & 1),
-                       desc_mn<BN>(sm.kv[ring.slot]), id_o, j == 0);
-          mma_commit(&sm.pv_done);
-          mma_commit(&sm.empty[ring.slot]);
-          ring.next();
-          // its arrival also says that P V of run j is done: P's buffer is free for run j + 2
-          if (j + 2 < n) scores(j & 1);
-        }
-        mma_commit(&sm.o_full);
-      }
-      __syncwarp();
     }
+    __syncwarp();
     tc_fence_before();
     named_barrier_sync(15, kThreads64);
     tc_fence_after();
-    if (warp == kMmaWarp64) tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 128);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs64));
     const int r = threadIdx.x;
     const uint32_t lane_base = tmem + ((warp * 32u) << 16);
     const uint32_t o_at = lane_base + kColO64;
@@ -606,12 +590,11 @@ __global__ void __launch_bounds__(kThreads64, 2)
 
     auto block = [&](int j, auto masked) {
       constexpr bool MASK = decltype(masked)::value;
-      const uint32_t s_at = lane_base + BN * (j & 1), p_at = lane_base + kColP64 + 32 * (j & 1);
-      mbar_wait(&sm.s_full[j & 1], (j >> 1) & 1, 350);
+      mbar_wait(&sm.s_full, j & 1, 350);
       tc_fence_after();
       uint32_t x[2][32];
-      tmem_ld32(s_at, x[0]);
-      tmem_ld32(s_at + 32, x[1]);
+      tmem_ld32(lane_base, x[0]);
+      tmem_ld32(lane_base + 32, x[1]);
       tmem_ld_wait_regs32(x[0]);
       tie32(x[1]);
       if (MASK) {
@@ -640,43 +623,41 @@ __global__ void __launch_bounds__(kThreads64, 2)
         const float alpha = grow ? ex2_approx(m - mn) : 1.0f;
         m = mn;
         l *= alpha;
-        if (j > 0) {
-          mbar_wait(&sm.pv_done, (j - 1) & 1, 351);  // O is up to date
-          tc_fence_after();
+        if (j > 0) {  // O is up to date: S of this run was issued after P V of the last
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 8) {  // few registers: x is live
+            uint32_t y[8], none[8] = {};
+            tmem_ld8(o_at + cc, y);
+            tmem_ld_wait_regs8(y, none);
 #pragma unroll
-          for (int cc = 0; cc < D; cc += 16) {
-            uint32_t y[16];
-            tmem_ld16(o_at + cc, y);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              asm volatile("" : "+r"(y[e]));
+            for (int e = 0; e < 8; ++e)
               y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
-            }
-            tmem_st16(o_at + cc, y);
+            tmem_st8(o_at + cc, y);
           }
         }
       }
       const float neg = m == -INFINITY ? 0.0f : -m;
       const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
       float2 sum = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
-      uint32_t w[32];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int q = k >> 4, e = 2 * (k & 15);
-        const float2 z = __ffma2_rn(
-            make_float2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])), c2, n2);
-        const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-        if (k & 1)
-          sum2 = __fadd2_rn(sum2, p);
-        else
-          sum = __fadd2_rn(sum, p);
-        w[k] = Cvt<T>::pack2(p.x, p.y);
+      for (int q = 0; q < 2; ++q) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float2 z = __ffma2_rn(
+              make_float2(__uint_as_float(x[q][2 * k]), __uint_as_float(x[q][2 * k + 1])), c2, n2);
+          const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+          if (k & 1)
+            sum2 = __fadd2_rn(sum2, p);
+          else
+            sum = __fadd2_rn(sum, p);
+          w[k] = Cvt<T>::pack2(p.x, p.y);
+        }
+        tmem_st16(lane_base + 16 * q, w);
       }
-      tmem_st32(p_at, w);
       tmem_st_wait();  // of O too, where it was rescaled
       tc_fence_before();
-      mbar_arrive(&sm.p_full[j & 1]);
+      mbar_arrive(&sm.p_full);
       l += (sum.x + sum.y) + (sum2.x + sum2.y);
     };
     for (int j = 0; j < n; ++j) {
