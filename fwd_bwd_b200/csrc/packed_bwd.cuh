@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
-      if (lane == 0) {
+      {
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
         constexpr uint32_t id_g = instr_desc(1, kFmt, kFmt, false, true, BT, D);
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           mbar_wait(&sm.full[at.slot], at.parity, 411);
           tc_fence_after();
           mma_rows<D, BN>(tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
-          mma_commit(bar);
+          mma_commit_warp(bar);
         };
         Ring<NST> q_at, do_at;  // of Q_n and dO_n
         do_at.next();
@@ -346,16 +346,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           tc_fence_after();
           // dV += P^T dO
           mma_sum<C::kWG>(tmem + kColDV, tmem, desc_mn<BN>(sm.ring[do_slot]), id_g, n == 0);
-          mma_commit(&sm.empty[do_slot]);
+          mma_commit_warp(&sm.empty[do_slot]);
           if (more) product(0, k_desc, q_at, &sm.s_full);
           mbar_wait(&sm.ds_ready, n & 1, 413);
           tc_fence_after();
           // dK += dS^T Q
           mma_sum<C::kWG>(tmem + kColDK, tmem + kColDP, desc_mn<BN>(sm.ring[q_slot]), id_g, n == 0);
-          mma_commit(&sm.empty[q_slot]);
+          mma_commit_warp(&sm.empty[q_slot]);
           if (more) product(kColDP, v_desc, do_at, &sm.dp_full);
         }
-        mma_commit(&sm.done);
+        mma_commit_warp(&sm.done);
       }
       __syncwarp();
     }
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
-      if (lane == 0) {
+      {
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
         constexpr uint32_t id_g = instr_desc(1, kFmt, kFmt, false, true, BT, D);
@@ -577,14 +577,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           mbar_wait(&sm.full[at.slot], at.parity, 511);
           tc_fence_after();
           mma_rows<D, BN>(tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
-          mma_commit(bar);
+          mma_commit_warp(bar);
         };
         Ring<NST> s_at, v_at, k_at;  // K of the next S, V of the next dP, K of the next dQ
         v_at.next();
         mbar_wait(&sm.q_full, 0, 510);
         product(0, q_desc, s_at, &sm.s_full[0]);
         product(kColDP, do_desc, v_at, &sm.dp_full);
-        mma_commit(&sm.empty[v_at.slot]);
+        mma_commit_warp(&sm.empty[v_at.slot]);
         s_at.next();
         s_at.next();
         v_at.next();
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           if (n + 1 < n_all) {  // dP of the next run once this one's has been read
             mbar_wait(&sm.dp_free, n & 1, 512);
             product(kColDP, do_desc, v_at, &sm.dp_full);
-            mma_commit(&sm.empty[v_at.slot]);
+            mma_commit_warp(&sm.empty[v_at.slot]);
             v_at.next();
             v_at.next();
           }
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           if (n >= pre)
             mma_sum<C::kWG>(tmem + kColDQ, tmem + BN * (n & 1), desc_mn<BN>(sm.ring[k_at.slot]),
                             id_g, n == pre);
-          mma_commit(&sm.empty[k_at.slot]);
+          mma_commit_warp(&sm.empty[k_at.slot]);
           k_at.next();
           k_at.next();
           if (n + 2 < n_all) {
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
             s_at.next();
           }
         }
-        mma_commit(&sm.done);
+        mma_commit_warp(&sm.done);
       }
       __syncwarp();
     }
