@@ -150,11 +150,11 @@ __device__ __forceinline__ float ds_factor(const uint32_t* norms) {
 
 // D (+)= A B over the 64 WG rows of tile B, A in TMEM: 32 columns from every 64th.
 template <int WG>
-__device__ __forceinline__ void mma_sum(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+__device__ __forceinline__ void mma_sum(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
                                         uint32_t idesc, bool start) {
 #pragma unroll
   for (int h = 0; h < WG; ++h)
-    mma_sum_half(d_tmem, a_tmem + 64 * h, b + step_mn(4 * h), idesc, start && h == 0);
+    mma_sum_half(leader, d_tmem, a_tmem + 64 * h, b + step_mn(4 * h), idesc, start && h == 0);
 }
 
 struct Args {
@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
       {
+        const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
         constexpr uint32_t id_g = instr_desc(1, kFmt, kFmt, false, true, BT, D);
@@ -327,8 +328,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
         auto product = [&](uint32_t col, uint64_t rows, const Ring<NST>& at, uint64_t* bar) {
           mbar_wait(&sm.full[at.slot], at.parity, 411);
           tc_fence_after();
-          mma_rows<D, BN>(tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
-          mma_commit_warp(bar);
+          mma_rows<D, BN>(leader, tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
+          mma_commit_warp(leader, bar);
         };
         Ring<NST> q_at, do_at;  // of Q_n and dO_n
         do_at.next();
@@ -345,17 +346,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           mbar_wait(&sm.p_ready, n & 1, 412);
           tc_fence_after();
           // dV += P^T dO
-          mma_sum<C::kWG>(tmem + kColDV, tmem, desc_mn<BN>(sm.ring[do_slot]), id_g, n == 0);
-          mma_commit_warp(&sm.empty[do_slot]);
+          mma_sum<C::kWG>(leader, tmem + kColDV, tmem, desc_mn<BN>(sm.ring[do_slot]), id_g, n == 0);
+          mma_commit_warp(leader, &sm.empty[do_slot]);
           if (more) product(0, k_desc, q_at, &sm.s_full);
           mbar_wait(&sm.ds_ready, n & 1, 413);
           tc_fence_after();
           // dK += dS^T Q
-          mma_sum<C::kWG>(tmem + kColDK, tmem + kColDP, desc_mn<BN>(sm.ring[q_slot]), id_g, n == 0);
-          mma_commit_warp(&sm.empty[q_slot]);
+          mma_sum<C::kWG>(leader, tmem + kColDK, tmem + kColDP, desc_mn<BN>(sm.ring[q_slot]), id_g, n == 0);
+          mma_commit_warp(leader, &sm.empty[q_slot]);
           if (more) product(kColDP, v_desc, do_at, &sm.dp_full);
         }
-        mma_commit_warp(&sm.done);
+        mma_commit_warp(leader, &sm.done);
       }
       __syncwarp();
     }
@@ -569,6 +570,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
       {
+        const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
         constexpr uint32_t id_g = instr_desc(1, kFmt, kFmt, false, true, BT, D);
@@ -576,15 +578,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
         auto product = [&](uint32_t col, uint64_t rows, const Ring<NST>& at, uint64_t* bar) {
           mbar_wait(&sm.full[at.slot], at.parity, 511);
           tc_fence_after();
-          mma_rows<D, BN>(tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
-          mma_commit_warp(bar);
+          mma_rows<D, BN>(leader, tmem + col, rows, desc_k(sm.ring[at.slot]), id_s);
+          mma_commit_warp(leader, bar);
         };
         Ring<NST> s_at, v_at, k_at;  // K of the next S, V of the next dP, K of the next dQ
         v_at.next();
         mbar_wait(&sm.q_full, 0, 510);
         product(0, q_desc, s_at, &sm.s_full[0]);
         product(kColDP, do_desc, v_at, &sm.dp_full);
-        mma_commit_warp(&sm.empty[v_at.slot]);
+        mma_commit_warp(leader, &sm.empty[v_at.slot]);
         s_at.next();
         s_at.next();
         v_at.next();
@@ -598,7 +600,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           if (n + 1 < n_all) {  // dP of the next run once this one's has been read
             mbar_wait(&sm.dp_free, n & 1, 512);
             product(kColDP, do_desc, v_at, &sm.dp_full);
-            mma_commit_warp(&sm.empty[v_at.slot]);
+            mma_commit_warp(leader, &sm.empty[v_at.slot]);
             v_at.next();
             v_at.next();
           }
@@ -606,9 +608,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           tc_fence_after();
           // dQ += dS K
           if (n >= pre)
-            mma_sum<C::kWG>(tmem + kColDQ, tmem + BN * (n & 1), desc_mn<BN>(sm.ring[k_at.slot]),
+            mma_sum<C::kWG>(leader, tmem + kColDQ, tmem + BN * (n & 1), desc_mn<BN>(sm.ring[k_at.slot]),
                             id_g, n == pre);
-          mma_commit_warp(&sm.empty[k_at.slot]);
+          mma_commit_warp(leader, &sm.empty[k_at.slot]);
           k_at.next();
           k_at.next();
           if (n + 2 < n_all) {
@@ -617,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
             s_at.next();
           }
         }
-        mma_commit_warp(&sm.done);
+        mma_commit_warp(leader, &sm.done);
       }
       __syncwarp();
     }

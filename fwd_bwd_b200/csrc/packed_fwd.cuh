@@ -137,17 +137,17 @@ __host__ __device__ constexpr uint32_t step_mn(int kk) { return (kk * 16 * 128) 
 
 // D = A B^T over D channels, K-major tiles of 128 and N rows.  (These are for a whole warp.)
 template <int D, int N>
-__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_rows(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk)
-    mma_f16_warp(d_tmem, a + step_k<BT>(kk), b + step_k<N>(kk), idesc, kk > 0 ? 1u : 0u);
+    mma_f16_warp(leader, d_tmem, a + step_k<BT>(kk), b + step_k<N>(kk), idesc, kk > 0 ? 1u : 0u);
 }
 // D (+)= A B over 64 rows of tile B, A in 32 TMEM columns.
-__device__ __forceinline__ void mma_sum_half(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+__device__ __forceinline__ void mma_sum_half(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
                                              uint32_t idesc, bool start) {
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk)
-    mma_f16_ts_warp(d_tmem, a_tmem + 8 * kk, b + step_mn(kk), idesc, kk > 0 || !start ? 1u : 0u);
+    mma_f16_ts_warp(leader, d_tmem, a_tmem + 8 * kk, b + step_mn(kk), idesc, kk > 0 || !start ? 1u : 0u);
 }
 
 // Position in a ring of N buffers, and the parity of the buffer's current round.
@@ -287,13 +287,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == kMmaWarp) {
       {
+        const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
         constexpr uint32_t id_o = instr_desc(1, kFmt, kFmt, false, true, BT, D);
         const uint64_t q_desc[2] = {desc_k(sm.q[0]), desc_k(sm.q[1])};
         auto scores = [&](int g, uint64_t k_desc) {  // S_g = Q_g K^T
-          mma_rows<D, BT>(tmem + 128 * g, q_desc[g], k_desc, id_s);
-          mma_commit_warp(&sm.s_full[g]);
+          mma_rows<D, BT>(leader, tmem + 128 * g, q_desc[g], k_desc, id_s);
+          mma_commit_warp(leader, &sm.s_full[g]);
         };
         auto values = [&](int g, uint64_t v_desc, int j) {  // O_g += P_g V
           // in halves of the keys, so that the first runs during the second's exponentials
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2; ++h) {
             mbar_wait(&sm.p_full[g][h], j & 1, 312);
             tc_fence_after();
-            mma_sum_half(tmem + kColO + D * g, tmem + 128 * g + 32 * h, v_desc + step_mn(4 * h),
+            mma_sum_half(leader, tmem + kColO + D * g, tmem + 128 * g + 32 * h, v_desc + step_mn(4 * h),
                          id_o, j == 0 && h == 0);
           }
         };
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         scores(0, desc_k(sm.kv[0]));
         if (n1 > 0) scores(1, desc_k(sm.kv[0]));
-        mma_commit_warp(&sm.empty[0]);
+        mma_commit_warp(leader, &sm.empty[0]);
         ring.next();
         for (int j = 0; j < n0; ++j) {
           const bool more = j + 1 < n0;
@@ -332,10 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             values(g, v_desc, j);
             if (j + 1 < n) scores(g, k_desc);
           }
-          mma_commit_warp(&sm.empty[v_slot]);
-          if (more) mma_commit_warp(&sm.empty[k_slot]);
+          mma_commit_warp(leader, &sm.empty[v_slot]);
+          if (more) mma_commit_warp(leader, &sm.empty[k_slot]);
         }
-        mma_commit_warp(&sm.o_full);
+        mma_commit_warp(leader, &sm.o_full);
       }
       __syncwarp();
     }
@@ -535,15 +536,16 @@ __global__ void __launch_bounds__(kThreads64, 4)
 
   if (warp == kIssueWarp64) {
     {
+      const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
       constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
       constexpr uint32_t id_o = instr_desc(1, kFmt, kFmt, false, true, BT, D);
       auto load = [&](T* dst, const CUtensorMap* map, int j, uint64_t* bar) {
-        if (j >= n || !elect_one()) return;
+        if (j >= n || !leader) return;
         mbar_arrive_expect_tx(bar, BN * D * 2);
         load_tile<T, D, BN, BN>(dst, map, it, first + j, kv_head, bar);
       };
-      if (elect_one()) {
+      if (leader) {
         mbar_arrive_expect_tx(&sm.q_full, BT * D * 2);
         load_tile<T, D, BN, BT>(sm.q, &tm_q, it, it.tile, head, &sm.q_full);
       }
@@ -557,8 +559,8 @@ __global__ void __launch_bounds__(kThreads64, 4)
       mbar_wait(&sm.q_full, 0, 340);
       mbar_wait(&sm.k_full[0], 0, 341);
       tc_fence_after();
-      mma_rows<D, BN>(tmem, q_desc, k_desc[0], id_s);
-      mma_commit_warp(&sm.s_full);
+      mma_rows<D, BN>(leader, tmem, q_desc, k_desc[0], id_s);
+      mma_commit_warp(leader, &sm.s_full);
       for (int j = 0; j < n; ++j) {
         const int b = j & 1, nb = b ^ 1;
         const uint32_t parity = (j >> 1) & 1;
@@ -566,12 +568,12 @@ __global__ void __launch_bounds__(kThreads64, 4)
         if (j + 1 < n) mbar_wait(&sm.k_full[nb], ((j + 1) >> 1) & 1, 341);
         mbar_wait(&sm.p_full, j & 1, 343);
         tc_fence_after();
-        mma_sum_half(tmem + kColO64, tmem, v_desc[b], id_o, j == 0);  // O += P V
+        mma_sum_half(leader, tmem + kColO64, tmem, v_desc[b], id_o, j == 0);  // O += P V
         if (j + 1 < n) {
-          mma_rows<D, BN>(tmem, q_desc, k_desc[nb], id_s);
-          mma_commit_warp(&sm.s_full);
+          mma_rows<D, BN>(leader, tmem, q_desc, k_desc[nb], id_s);
+          mma_commit_warp(leader, &sm.s_full);
         } else {
-          mma_commit_warp(&sm.o_full);
+          mma_commit_warp(leader, &sm.o_full);
         }
         // P of run j has arrived: S of run j and P V of run j - 1 are complete
         load(sm.v[nb], &tm_v, j + 1, &sm.v_full[nb]);

@@ -250,30 +250,30 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
-// Forms for a whole converged warp, one elected lane (always the same) issuing: the operands are
-// then warp-uniform values in uniform registers.  Issued from a branch of one lane, each
+// Forms for a whole converged warp, one lane (leader != 0 there, from elect_one) issuing: the
+// operands are then warp-uniform values in uniform registers.  Issued from a branch of one lane, each
 // instruction moves them there first, and a chain of short MMAs waits for that (~100 cycles an
 // instruction; M = 128, N = K = 64 computes in 128).
-__device__ __forceinline__ void mma_f16_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+__device__ __forceinline__ void mma_f16_warp(uint32_t leader, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                              uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
 // A in TMEM: lane = row, each 32-bit column two consecutive elements along K (8 columns per K =
 // 16).
-__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+__device__ __forceinline__ void mma_f16_ts_warp(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                                 uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
 
@@ -308,13 +308,13 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
       : "memory");
 }
 
-// For a whole converged warp: the lane that the warp forms above elect.
-__device__ __forceinline__ void mma_commit_warp(uint64_t* bar) {
+// Likewise; the leader must be the one that issued the MMAs.
+__device__ __forceinline__ void mma_commit_warp(uint32_t leader, uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          smem_u32(bar))
+          smem_u32(bar)), "r"(leader)
       : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
@@ -326,6 +326,8 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(r));
   return r != 0;
 }
+// A value that all lanes hold, in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
 // Each thread of the warp reads 16 consecutive 32-bit columns of its own TMEM lane.
 // The warp may only address its lane quarter: lanes 32*(warp_id % 4) .. +31.
