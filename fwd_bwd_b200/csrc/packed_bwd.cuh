@@ -261,13 +261,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       mbar_init(&sm.empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sm.vec_full[s], 32);
-      mbar_init(&sm.vec_empty[s], C::kCompute);
+      mbar_init(&sm.vec_full[s], 1);
+      mbar_init(&sm.vec_empty[s], C::kCompute / 32);
     }
     mbar_init(&sm.s_full, 1);
     mbar_init(&sm.dp_full, 1);
-    mbar_init(&sm.p_ready, C::kCompute);
-    mbar_init(&sm.ds_ready, C::kCompute);
+    mbar_init(&sm.p_ready, C::kCompute / 32);
+    mbar_init(&sm.ds_ready, C::kCompute / 32);
     mbar_init(&sm.done, 1);
     fence_barrier_init();
   }
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           sm.lse[b][r] = i >= 0 ? fmaf(a.lse[base + i], kLog2e, -Scaling<T>::kPShift) : INFINITY;
           sm.dvec[b][r] = i >= 0 ? a.dvec[base + i] : 0.0f;
         }
-        mbar_arrive(&sm.vec_full[b]);
+        mbar_arrive_warp(&sm.vec_full[b], lane);
       }
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sm.p_ready);
+      mbar_arrive_warp(&sm.p_ready, lane);
       // dS = P (dP - D)
       mbar_wait(&sm.dp_full, n & 1, 422);
       tc_fence_after();
@@ -432,8 +432,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sm.ds_ready);
-      mbar_arrive(&sm.vec_empty[b]);
+      mbar_arrive_warp(&sm.ds_ready, lane);
+      mbar_arrive_warp(&sm.vec_empty[b], lane);
     };
     Walk at = begin;
     for (int n = 0; n < n_all; ++n, at.next()) {
@@ -530,10 +530,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     mbar_init(&sm.s_full[0], 1);
     mbar_init(&sm.s_full[1], 1);
     mbar_init(&sm.dp_full, 1);
-    mbar_init(&sm.dp_free, C::kCompute);
+    mbar_init(&sm.dp_free, C::kCompute / 32);
     // two, because dP of the next run is issued before this one's dS is waited for
-    mbar_init(&sm.ds_ready[0], C::kCompute);
-    mbar_init(&sm.ds_ready[1], C::kCompute);
+    mbar_init(&sm.ds_ready[0], C::kCompute / 32);
+    mbar_init(&sm.ds_ready[1], C::kCompute / 32);
     mbar_init(&sm.done, 1);
     fence_barrier_init();
   }
@@ -676,8 +676,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
                              make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), sum);
         }
         tc_fence_before();
-        mbar_arrive(&sm.dp_free);
-        mbar_arrive(&sm.ds_ready[n & 1]);
+        mbar_arrive_warp(&sm.dp_free, lane);
+        mbar_arrive_warp(&sm.ds_ready[n & 1], lane);
         dvec += (sum.x + sum.y) * exp2f(-Scaling<T>::kPShift);
         if (n == pre - 1) {
           if (C::kWG == 2) {
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
         tmem_ld_wait_regs32(y);
         if (h == 1) {
           tc_fence_before();
-          mbar_arrive(&sm.dp_free);
+          mbar_arrive_warp(&sm.dp_free, lane);
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sm.ds_ready[n & 1]);
+      mbar_arrive_warp(&sm.ds_ready[n & 1], lane);
     };
     for (int n = 0; n < n_all; ++n) {
       const int run = run_of(n);

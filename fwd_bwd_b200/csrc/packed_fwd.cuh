@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sm.s_full[g], 1);
-      mbar_init(&sm.p_full[g][0], 128);
-      mbar_init(&sm.p_full[g][1], 128);
+      mbar_init(&sm.p_full[g][0], 4);
+      mbar_init(&sm.p_full[g][1], 4);
     }
     mbar_init(&sm.o_full, 1);
     fence_barrier_init();
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st32(s_at + 32 * hh, w);
         tmem_st_wait();  // of O too, where it was rescaled
         tc_fence_before();
-        mbar_arrive(&sm.p_full[g][hh]);
+        mbar_arrive_warp(&sm.p_full[g][hh], lane);
       }
       l += (sum.x + sum.y) + (sum2.x + sum2.y);
     };
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads64, 4)
       mbar_init(&sm.v_full[s], 1);
     }
     mbar_init(&sm.s_full, 1);
-    mbar_init(&sm.p_full, 128);
+    mbar_init(&sm.p_full, 4);
     mbar_init(&sm.o_full, 1);
     fence_barrier_init();
   }
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kThreads64, 4)
       }
       tmem_st_wait();  // of O too, where it was rescaled
       tc_fence_before();
-      mbar_arrive(&sm.p_full);
+      mbar_arrive_warp(&sm.p_full, lane);
       l += (sum.x + sum.y) + (sum2.x + sum2.y);
     };
     for (int j = 0; j < n; ++j) {
