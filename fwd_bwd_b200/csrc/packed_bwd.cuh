@@ -169,17 +169,17 @@ struct Args {
   float scale_log2, tau;
 };
 
-// P (times 2^shift) of 64 columns from the scores x, in place: z = x c - shift(e).
-// MASK: columns for which hidden(e) holds are zero.
-template <bool MASK, bool POLY, typename Shift, typename Hidden>
-__device__ __forceinline__ void probabilities(uint32_t (&x)[2][32], float c, Shift shift,
+// P (times 2^shift) of 32 columns from the scores x, in place: z = x c + offset(e).
+// MASK: columns for which hidden(e) holds are zero.  POLY: a quarter of the exponentials on the
+// FMA pipe.
+template <bool MASK, bool POLY, typename Offset, typename Hidden>
+__device__ __forceinline__ void probabilities(uint32_t (&x)[32], float c, Offset offset,
                                               Hidden hidden) {
   const float2 c2 = make_float2(c, c);
 #pragma unroll
-  for (int e = 0; e < 64; e += 2) {
-    uint32_t& x0 = x[e >> 5][e & 31];
-    uint32_t& x1 = x[e >> 5][(e & 31) + 1];
-    float2 z = __ffma2_rn(make_float2(__uint_as_float(x0), __uint_as_float(x1)), c2, shift(e));
+  for (int e = 0; e < 32; e += 2) {
+    float2 z = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2,
+                          offset(e));
     float2 p;
     if (MASK) {
       if (hidden(e)) z.x = -INFINITY;
@@ -190,9 +190,19 @@ __device__ __forceinline__ void probabilities(uint32_t (&x)[2][32], float c, Shi
     } else {
       p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
     }
-    x0 = __float_as_uint(p.x);
-    x1 = __float_as_uint(p.y);
+    x[e] = __float_as_uint(p.x);
+    x[e + 1] = __float_as_uint(p.y);
   }
+}
+template <typename T>
+__device__ __forceinline__ void pack32(const uint32_t (&x)[32], uint32_t (&w)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    w[e] = Cvt<T>::pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+}
+// Two neighbouring values of a shared-memory vector, four of which are loaded together.
+__device__ __forceinline__ float2 pair_of(const float4& v, int e) {
+  return (e & 2) ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
 }
 
 // ---- dK and dV ------------------------------------------------------------------------------
@@ -203,10 +213,11 @@ struct DkvSmem {
   alignas(1024) T k[BT * D];
   alignas(1024) T v[BT * D];
   alignas(1024) T ring[NST][BN * D];
-  alignas(16) float lse[2][BN];  // LSE log2 e - P's shift of the query rows, +inf: padding
-  alignas(16) float dvec[2][BN];
+  // of the query rows, negated: LSE log2 e - P's shift (-inf for padding: P = 0), and D
+  alignas(16) float neg_lse[2][BN];
+  alignas(16) float neg_d[2][BN];
   uint64_t kv_full, full[NST], empty[NST], vec_full[2], vec_empty[2];
-  uint64_t s_full, dp_full, p_ready, ds_ready, done;
+  uint64_t s_full, dp_full, p_ready[2], ds_ready, done;
   uint32_t tmem_base;
   int abort;
 };
@@ -266,7 +277,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     }
     mbar_init(&sm.s_full, 1);
     mbar_init(&sm.dp_full, 1);
-    mbar_init(&sm.p_ready, C::kCompute / 32);
+    mbar_init(&sm.p_ready[0], C::kCompute / 32);
+    mbar_init(&sm.p_ready[1], C::kCompute / 32);
     mbar_init(&sm.ds_ready, C::kCompute / 32);
     mbar_init(&sm.done, 1);
     fence_barrier_init();
@@ -312,8 +324,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
 #pragma unroll
         for (int r = lane; r < BN; r += 32) {
           const int i = row_index<BN>(it, at.run, r);
-          sm.lse[b][r] = i >= 0 ? fmaf(a.lse[base + i], kLog2e, -Scaling<T>::kPShift) : INFINITY;
-          sm.dvec[b][r] = i >= 0 ? a.dvec[base + i] : 0.0f;
+          sm.neg_lse[b][r] =
+              i >= 0 ? fmaf(a.lse[base + i], -kLog2e, Scaling<T>::kPShift) : -INFINITY;
+          sm.neg_d[b][r] = i >= 0 ? -a.dvec[base + i] : 0.0f;
         }
         mbar_arrive_warp(&sm.vec_full[b], lane);
       }
@@ -343,10 +356,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           q_at.next();
           do_at.next();
           do_at.next();
-          mbar_wait(&sm.p_ready, n & 1, 412);
-          tc_fence_after();
-          // dV += P^T dO
-          mma_sum<C::kWG>(leader, tmem + kColDV, tmem, desc_mn<BN>(sm.ring[do_slot]), id_g, n == 0);
+          // dV += P^T dO, by quarters of 32 query rows (d = 64: halves): the first of every half
+          const uint64_t do_desc = desc_mn<BN>(sm.ring[do_slot]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            mbar_wait(&sm.p_ready[h], n & 1, 412);
+            tc_fence_after();
+#pragma unroll
+            for (int w = 0; w < C::kWG; ++w)
+              mma_sum_quarter(leader, tmem + kColDV, tmem + 64 * w + 16 * h,
+                              do_desc + step_mn(4 * w + 2 * h), id_g, n == 0 && w == 0 && h == 0);
+          }
           mma_commit_warp(leader, &sm.empty[do_slot]);
           if (more) product(0, k_desc, q_at, &sm.s_full);
           mbar_wait(&sm.ds_ready, n & 1, 413);
@@ -387,44 +407,44 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       tmem_ld32(s_at + 32, x[1]);
       tmem_ld_wait_regs32(x[0]);
       tie32(x[1]);
-      const float* lse = sm.lse[b] + 64 * half;
       // query row before the key's own position: hidden (the diagonal of a causal mask)
       const int hidden = r - (run - diag) * BN - 64 * half;  // columns below it
-      probabilities<MASK, true>(
-          x, c,
-          [&](int e) {
-            const float2 s = *reinterpret_cast<const float2*>(lse + e);
-            return make_float2(-s.x, -s.y);
-          },
-          [&](int e) { return e < hidden; });
+      // in halves, so that dV's products with the first run during the second's exponentials
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w[16];
+        float4 off[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          w[e] = Cvt<T>::pack2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1]));
+        for (int k = 0; k < 8; ++k)
+          off[k] = *reinterpret_cast<const float4*>(&sm.neg_lse[b][64 * half + 32 * h + 4 * k]);
+        probabilities<MASK, true>(
+            x[h], c, [&](int e) { return pair_of(off[e >> 2], e); },
+            [&](int e) { return 32 * h + e < hidden; });
+        uint32_t w[16];
+        pack32<T>(x[h], w);
         tmem_st16(s_at + 16 * h, w);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&sm.p_ready[h], lane);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive_warp(&sm.p_ready, lane);
       // dS = P (dP - D)
       mbar_wait(&sm.dp_full, n & 1, 422);
       tc_fence_after();
-      const float* dv = sm.dvec[b] + 64 * half;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t y[32], w[16];
         tmem_ld32(dp_at + 32 * h, y);
+        float4 off[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          off[k] = *reinterpret_cast<const float4*>(&sm.neg_d[b][64 * half + 32 * h + 4 * k]);
         tmem_ld_wait_regs32(y);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float2 d2 = *reinterpret_cast<const float2*>(dv + 32 * h + 2 * e);
           float2 p = make_float2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1]));
           if (Scaling<T>::kOn) p = __fmul2_rn(p, make_float2(f_ds, f_ds));
           const float2 t =
               __fadd2_rn(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])),
-                         make_float2(-d2.x, -d2.y));
+                         pair_of(off[e >> 1], 2 * e));
           const float2 s = __fmul2_rn(p, t);
           w[e] = Cvt<T>::pack2(s.x, s.y);
         }
@@ -635,8 +655,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     const int i = row_index(it, it.tile, r);
     const int64_t row = static_cast<int64_t>(it.start) + i;
     // padding rows: P = exp2(-inf) = 0
-    const float shift =
-        i >= 0 ? fmaf(a.lse[head * a.T + row], kLog2e, -Scaling<T>::kPShift) : INFINITY;
+    const float neg_shift =
+        i >= 0 ? fmaf(a.lse[head * a.T + row], -kLog2e, Scaling<T>::kPShift) : -INFINITY;
     float dvec = i >= 0 && pre == 0 ? a.dvec[head * a.T + row] : 0.0f;
     const float c = a.scale_log2;
     float factor = 1.0f;
@@ -658,9 +678,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       tie32(x[1]);
       const int key0 = row_index<BN>(it, run_of(n), 64 * half);
       const int last = a.causal ? i : 0x7fffffff;
-      probabilities<MASK, false>(
-          x, c, [&](int) { return make_float2(-shift, -shift); },
-          [&](int e) { return key0 + e < 0 || key0 + e > last; });
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        probabilities<MASK, false>(
+            x[h], c, [&](int) { return make_float2(neg_shift, neg_shift); },
+            [&](int e) { return key0 + 32 * h + e < 0 || key0 + 32 * h + e > last; });
       mbar_wait(&sm.dp_full, n & 1, 521);
       tc_fence_after();
       if (n < pre) {  // D += P dP

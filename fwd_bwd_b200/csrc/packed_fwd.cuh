@@ -150,6 +150,15 @@ __device__ __forceinline__ void mma_sum_half(uint32_t leader, uint32_t d_tmem, u
     mma_f16_ts_warp(leader, d_tmem, a_tmem + 8 * kk, b + step_mn(kk), idesc, kk > 0 || !start ? 1u : 0u);
 }
 
+// The same over 32 rows.
+__device__ __forceinline__ void mma_sum_quarter(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
+                                                uint64_t b, uint32_t idesc, bool start) {
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk)
+    mma_f16_ts_warp(leader, d_tmem, a_tmem + 8 * kk, b + step_mn(kk), idesc,
+                    kk > 0 || !start ? 1u : 0u);
+}
+
 // Position in a ring of N buffers, and the parity of the buffer's current round.
 template <int N>
 struct Ring {
