@@ -107,8 +107,8 @@ void rope_args(const sage_rope_params* p, const sage_rows* q, const sage_rows* k
   a->pos = pos;
   a->tokens = p->B * p->N;
   a->N = p->N;
-  a->Hq = p->Hq;
-  a->H = p->Hq + p->Hkv;
+  a->heads[0] = p->Hq;
+  a->heads[1] = p->Hkv;
   a->rotary = p->rotary_dim;
   a->norm = p->norm;
   a->eps = p->eps;
@@ -120,15 +120,18 @@ void rope_args(const sage_rope_params* p, const sage_rows* q, const sage_rows* k
     for (int i = 0; i < p->rotary_dim / 2; ++i) a->freq[i] = turn_fraction(p->inv_freq[i]);
     for (int i = 0, at = 0; i + 1 < p->n_axes; ++i) a->bound[i] = at += p->sections[i];
   }
-  // Heads of a token per lane group: all of them when there are many times more tokens than
+  // Heads of a token per lane group: all of a tensor's when there are many times more tokens than
   // groups on the device (the angles are then computed once per token), fewer otherwise; a
   // multiple of the rows computed together.
   const int64_t want = 2 * 148 * 1024 / (p->d / 8);  // two rounds of lane groups
   const int64_t chunks = std::max<int64_t>(1, (want + a->tokens - 1) / a->tokens);
-  const int per = static_cast<int>(std::max<int64_t>(1, a->H / chunks));
-  a->per_chunk = per >= 4 ? per / 4 * 4 : per;
-  if (chunks == 1) a->per_chunk = a->H;
-  a->chunks = (a->H + a->per_chunk - 1) / a->per_chunk;
+  for (int w = 0; w < 2; ++w) {
+    const int H = a->heads[w];
+    const int per = static_cast<int>(std::max<int64_t>(1, (p->Hq + p->Hkv) / chunks));
+    a->per_chunk[w] = std::min(H, per >= 4 ? per / 4 * 4 : per);
+    if (chunks == 1) a->per_chunk[w] = H;
+    a->chunks[w] = (H + a->per_chunk[w] - 1) / a->per_chunk[w];
+  }
 }
 
 template <typename T, int D, bool INTER, bool BWD>
@@ -136,12 +139,21 @@ int run_rope(sage::rope::Args* a, float* dgain_q, float* dgain_k, cudaStream_t s
   const int groups = sage::rope::kThreads / (D / 8);
   const int sms = sm_count();
   if (sms == 0) return SAGE_ERR_CUDA;
-  const int64_t need = static_cast<int64_t>((a->tokens + groups - 1) / groups) * a->chunks;
   const int most = BWD ? std::min(kRopeBwdBlocks, 2 * sms) : 3 * sms;  // resident at once
-  const int blocks = static_cast<int>(std::min<int64_t>(need, most));
+  // q and k share them by their heads, and a token's angles and addresses at some rows' cost
+  constexpr int kUnitCost = 2;
+  const int64_t cost[2] = {a->heads[0] + kUnitCost * a->chunks[0],
+                           a->heads[1] + kUnitCost * a->chunks[1]};
+  const int64_t tiles = (a->tokens + groups - 1) / groups;
+  const int64_t share = most * cost[0] / (cost[0] + cost[1]);
+  const int for_q = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(share, most - 1)));
+  a->blocks_q = static_cast<int>(std::min<int64_t>(tiles * a->chunks[0], for_q));
+  const int blocks =
+      a->blocks_q + static_cast<int>(std::min<int64_t>(tiles * a->chunks[1], most - for_q));
   sage::rope::qk_rope_kernel<T, D, INTER, BWD><<<blocks, sage::rope::kThreads, 0, st>>>(*a);
   if (BWD && a->partial)
-    sage::rope::dgain_kernel<D><<<2 * D / 32, 1024, 0, st>>>(a->partial, blocks, dgain_q, dgain_k);
+    sage::rope::dgain_kernel<D><<<2 * D / 32, 1024, 0, st>>>(a->partial, a->blocks_q, blocks,
+                                                                 dgain_q, dgain_k);
   return launch_status();
 }
 
@@ -273,9 +285,12 @@ int launch_packed(K kern, int regs, int64_t grid, int threads, size_t smem, cuda
 // item takes, because the last chunk's long items start late (16384 tokens in documents of
 // 5021 to 2, 4 key heads, dK/dV: 330 us in one chunk, 442 us in four).
 constexpr int64_t kChunkBytes = 40 << 20;  // of the 126 MB L2
+constexpr int64_t kAllBytes = 80 << 20;    // what is this small in all stays there anyway
 int grid_chunk(const sage_packed_params* p, const sage_packed_info* info, int heads,
                int64_t bytes_per_head) {
-  const int64_t fit = kChunkBytes / std::max<int64_t>(bytes_per_head, 1);
+  const int64_t fit = heads * bytes_per_head <= kAllBytes
+                          ? heads
+                          : kChunkBytes / std::max<int64_t>(bytes_per_head, 1);
   const int64_t tiles = (static_cast<int64_t>(info->longest) + 127) / 128;  // the longest item
   const int64_t steps = std::max<int64_t>(p->causal ? info->causal_steps : info->full_steps, 1);
   const int64_t busy = (3 * 148 * tiles / 2 + steps - 1) / steps;  // 1.5 x the longest item
@@ -410,7 +425,7 @@ int sage_qk_norm_rope_fwd(const sage_rope_params* p, const sage_rows* q, const s
 
 size_t sage_qk_norm_rope_workspace_bytes(const sage_rope_params* p) {
   if (check_rope(p) != SAGE_OK) return 0;
-  return align_up(static_cast<size_t>(kRopeBwdBlocks) * 2 * p->d * 4);
+  return align_up(static_cast<size_t>(kRopeBwdBlocks) * p->d * 4);
 }
 
 int sage_qk_norm_rope_bwd(const sage_rope_params* p, const sage_rows* q, const sage_rows* k,

@@ -7,9 +7,9 @@
 // Bound: HBM (the forward moves 4 bytes per element, the backward 6).  Layout: a row of d
 // channels is held by d/8 lanes, each with two groups of 4 channels (two 8-byte loads): the two
 // halves of the same 4 pairs, so the rotation needs no exchange between lanes and a lane needs
-// 4 sines and cosines.  Such a group of lanes walks the heads of one token, q's and then k's,
-// because the angles depend on the token only, a few rows at a time so that their loads and their
-// row sums overlap.
+// 4 sines and cosines.  Such a group of lanes walks the heads of one token, because the angles
+// depend on the token only, a few rows at a time so that their loads and their row sums overlap.
+// The blocks are split between q and k by their heads (a warp never works on both).
 //
 // Angles: frequency i as F_i = inv_freq_i / (2 pi) * 2^64 modulo 2^64, so position * F_i
 // modulo 2^64 is the angle's fraction of a turn, with all full turns dropped exactly: the same
@@ -44,12 +44,14 @@ struct Args {
   Rows y[2];    // forward: outputs; backward: gradients of q, k
   const float* gain[2];
   const void* pos;
-  float* partial;  // backward: [blocks][2][D] sums of dgain, or null
+  float* partial;  // backward: [blocks][D] sums of dgain, or null
   int64_t pos_as, pos_bs;
   uint64_t freq[64];
   int bound[kMaxAxes - 1];  // first pair of axes 1, 2, 3
-  int tokens, N, Hq, H;     // H: heads of q and k
-  int chunks, per_chunk;    // the heads of a token are cut into `chunks` of per_chunk
+  int tokens, N;
+  int blocks_q;                 // blocks that work on q; the others work on k
+  int heads[2];
+  int chunks[2], per_chunk[2];  // the heads of a token are cut into `chunks` of per_chunk
   int rotary, pos64, norm;
   float eps;
 };
@@ -109,28 +111,51 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3)
     cv = cu + 4;
   }
   const int dv = cv - cu;
-  Pairs dgain[2];
+  Pairs dgain, gain;
 #pragma unroll
-  for (int w = 0; w < 2; ++w)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) dgain[w].a[i] = dgain[w].b[i] = make_float2(0.0f, 0.0f);
+  for (int i = 0; i < 2; ++i) {
+    dgain.a[i] = dgain.b[i] = make_float2(0.0f, 0.0f);
+    gain.a[i] = gain.b[i] = make_float2(1.0f, 1.0f);
+  }
+  const int w = static_cast<int>(blockIdx.x) >= a.blocks_q ? 1 : 0;
+  const int block = blockIdx.x - (w ? a.blocks_q : 0);
+  const int blocks = w ? gridDim.x - a.blocks_q : a.blocks_q;
+  const int chunks = a.chunks[w], per_chunk = a.per_chunk[w], H = a.heads[w];
+  if (a.gain[w]) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(a.gain[w] + cu));
+    const float4 v = __ldg(reinterpret_cast<const float4*>(a.gain[w] + cv));
+    if (INTER) {
+      gain.a[0] = make_float2(u.x, u.z);
+      gain.b[0] = make_float2(u.y, u.w);
+      gain.a[1] = make_float2(v.x, v.z);
+      gain.b[1] = make_float2(v.y, v.w);
+    } else {
+      gain.a[0] = make_float2(u.x, u.y);
+      gain.a[1] = make_float2(u.z, u.w);
+      gain.b[0] = make_float2(v.x, v.y);
+      gain.b[1] = make_float2(v.z, v.w);
+    }
+  }
+  const int64_t xs = a.x[w].hs, gs = a.g[w].hs, ys = a.y[w].hs;
 
-  // a block's unit: GROUPS tokens, one chunk of their heads (all lanes of a warp then work on the
-  // same tensor); neighbouring blocks take the same tokens' chunks
+  // a block's unit: GROUPS tokens, one chunk of their heads; neighbouring blocks take the same
+  // tokens' chunks
   const int tiles = (a.tokens + GROUPS - 1) / GROUPS;
-  const int64_t units = static_cast<int64_t>(tiles) * a.chunks;
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int tile = static_cast<int>(unit / a.chunks);
-    const int lo = static_cast<int>(unit - static_cast<int64_t>(tile) * a.chunks) * a.per_chunk;
-    const int hi = min(a.H, lo + a.per_chunk);
+  const int64_t units = static_cast<int64_t>(tiles) * chunks;
+  for (int64_t unit = block; unit < units; unit += blocks) {
+    const int tile = static_cast<int>(unit / chunks);
+    const int lo = static_cast<int>(unit - static_cast<int64_t>(tile) * chunks) * per_chunk;
+    const int hi = min(H, lo + per_chunk);
     const int token = tile * GROUPS + threadIdx.x / LPR;
     if (token >= a.tokens) continue;
     const int b = token < a.N ? 0 : token / a.N, n = token - b * a.N;
-    auto row_at = [&](const Rows (&r)[2], int h) {
-      const int w = h < a.Hq ? 0 : 1;
-      return reinterpret_cast<T*>(r[w].ptr) + b * r[w].bs + static_cast<int64_t>(n) * r[w].ts +
-             static_cast<int64_t>(h - (w ? a.Hq : 0)) * r[w].hs + cu;
+    auto row_at = [&](const Rows& r) {
+      return reinterpret_cast<T*>(r.ptr) + b * r.bs + static_cast<int64_t>(n) * r.ts +
+             static_cast<int64_t>(lo) * r.hs + cu;
     };
+    const T* xp = row_at(a.x[w]);
+    const T* gp = BWD ? row_at(a.g[w]) : nullptr;
+    T* yp = row_at(a.y[w]);
     int64_t at[4];  // the positions of the lane's pairs
     if (rot) {
 #pragma unroll
@@ -161,215 +186,183 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3)
       fresh = false;
     };
     int h = lo;
+    // R rows from h on
+    auto rows = [&](auto count) {
+      constexpr int R = decltype(count)::value;
+      uint2 xu[R], xv[R], gu[R], gv[R];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int end = w == 0 ? min(hi, a.Hq) : hi;
-      if (h >= end) continue;
-      const T* xp = row_at(a.x, h);
-      const T* gp = BWD ? row_at(a.g, h) : nullptr;
-      T* yp = row_at(a.y, h);
-      const int64_t xs = a.x[w].hs, gs = a.g[w].hs, ys = a.y[w].hs;
-      Pairs gain;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) gain.a[i] = gain.b[i] = make_float2(1.0f, 1.0f);
-      if (a.gain[w]) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(a.gain[w] + cu));
-        const float4 v = __ldg(reinterpret_cast<const float4*>(a.gain[w] + cv));
-        if (INTER) {
-          gain.a[0] = make_float2(u.x, u.z);
-          gain.b[0] = make_float2(u.y, u.w);
-          gain.a[1] = make_float2(v.x, v.z);
-          gain.b[1] = make_float2(v.y, v.w);
-        } else {
-          gain.a[0] = make_float2(u.x, u.y);
-          gain.a[1] = make_float2(u.z, u.w);
-          gain.b[0] = make_float2(v.x, v.y);
-          gain.b[1] = make_float2(v.z, v.w);
+      for (int i = 0; i < R; ++i) {
+        xu[i] = __ldcs(reinterpret_cast<const uint2*>(xp));
+        xv[i] = __ldcs(reinterpret_cast<const uint2*>(xp + dv));
+        xp += xs;
+        if (BWD) {
+          gu[i] = __ldcs(reinterpret_cast<const uint2*>(gp));
+          gv[i] = __ldcs(reinterpret_cast<const uint2*>(gp + dv));
+          gp += gs;
         }
       }
-      // R rows from h on
-      auto rows = [&](auto count) {
-        constexpr int R = decltype(count)::value;
-        uint2 xu[R], xv[R], gu[R], gv[R];
+      if (fresh) angles();
+      if (!BWD) {
+        float inv[R];
+        if (a.norm) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const Pairs x = unpack<T, INTER>(xu[i], xv[i]);
+            float2 ss = __fmul2_rn(x.a[0], x.a[0]);
+            ss = __ffma2_rn(x.b[0], x.b[0], ss);
+            ss = __ffma2_rn(x.a[1], x.a[1], ss);
+            ss = __ffma2_rn(x.b[1], x.b[1], ss);
+            inv[i] = ss.x + ss.y;
+          }
+#pragma unroll
+          for (int o = LPR / 2; o >= 1; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < R; ++i) inv[i] += __shfl_xor_sync(mask, inv[i], o);
+#pragma unroll
+          for (int i = 0; i < R; ++i) inv[i] = rsqrtf(fmaf(inv[i], 1.0f / D, a.eps));
+        }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-          xu[i] = __ldcs(reinterpret_cast<const uint2*>(xp));
-          xv[i] = __ldcs(reinterpret_cast<const uint2*>(xp + dv));
-          xp += xs;
-          if (BWD) {
-            gu[i] = __ldcs(reinterpret_cast<const uint2*>(gp));
-            gv[i] = __ldcs(reinterpret_cast<const uint2*>(gp + dv));
-            gp += gs;
+          Pairs x = unpack<T, INTER>(xu[i], xv[i]);
+          if (a.norm) {
+            const float2 inv2 = make_float2(inv[i], inv[i]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              x.a[k] = __fmul2_rn(__fmul2_rn(x.a[k], inv2), gain.a[k]);
+              x.b[k] = __fmul2_rn(__fmul2_rn(x.b[k], inv2), gain.b[k]);
+            }
+          }
+          if (rot) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float2 p = x.a[k], q = x.b[k];
+              x.a[k] = __ffma2_rn(p, cs[k], __fmul2_rn(q, ns[k]));
+              x.b[k] = __ffma2_rn(q, cs[k], __fmul2_rn(p, sn[k]));
+            }
+          }
+          uint2 u, v;
+          pack<T, INTER>(x, u, v);
+          *reinterpret_cast<uint2*>(yp) = u;
+          *reinterpret_cast<uint2*>(yp + dv) = v;
+          yp += ys;
+        }
+      } else {
+        Pairs g[R];
+        float2 sums[R];  // of x^2 and of gx x: xhat = x inv, inv known only after them
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          g[i] = unpack<T, INTER>(gu[i], gv[i]);
+          if (rot) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float2 p = g[i].a[k], q = g[i].b[k];
+              g[i].a[k] = __ffma2_rn(p, cs[k], __fmul2_rn(q, sn[k]));
+              g[i].b[k] = __ffma2_rn(q, cs[k], __fmul2_rn(p, ns[k]));
+            }
+          }
+          if (a.norm) {
+            const Pairs x = unpack<T, INTER>(xu[i], xv[i]);
+            float2 ss = make_float2(0.0f, 0.0f), dot = ss;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              ss = __ffma2_rn(x.a[k], x.a[k], __ffma2_rn(x.b[k], x.b[k], ss));
+              dot = __ffma2_rn(__fmul2_rn(g[i].a[k], gain.a[k]), x.a[k], dot);
+              dot = __ffma2_rn(__fmul2_rn(g[i].b[k], gain.b[k]), x.b[k], dot);
+            }
+            sums[i] = make_float2(ss.x + ss.y, dot.x + dot.y);
           }
         }
-        if (fresh) angles();
-        if (!BWD) {
-          float inv[R];
+        if (a.norm) {
+#pragma unroll
+          for (int o = LPR / 2; o >= 1; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+              sums[i] = __fadd2_rn(sums[i], make_float2(__shfl_xor_sync(mask, sums[i].x, o),
+                                                        __shfl_xor_sync(mask, sums[i].y, o)));
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
           if (a.norm) {
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-              const Pairs x = unpack<T, INTER>(xu[i], xv[i]);
-              float2 ss = __fmul2_rn(x.a[0], x.a[0]);
-              ss = __ffma2_rn(x.b[0], x.b[0], ss);
-              ss = __ffma2_rn(x.a[1], x.a[1], ss);
-              ss = __ffma2_rn(x.b[1], x.b[1], ss);
-              inv[i] = ss.x + ss.y;
-            }
-#pragma unroll
-            for (int o = LPR / 2; o >= 1; o >>= 1)
-#pragma unroll
-              for (int i = 0; i < R; ++i) inv[i] += __shfl_xor_sync(mask, inv[i], o);
-#pragma unroll
-            for (int i = 0; i < R; ++i) inv[i] = rsqrtf(fmaf(inv[i], 1.0f / D, a.eps));
-          }
-#pragma unroll
-          for (int i = 0; i < R; ++i) {
             Pairs x = unpack<T, INTER>(xu[i], xv[i]);
-            if (a.norm) {
-              const float2 inv2 = make_float2(inv[i], inv[i]);
+            const float inv = rsqrtf(fmaf(sums[i].x, 1.0f / D, a.eps));
+            // xhat mean(gx xhat) = xhat * (mean(gx x) inv)
+            const float mean = sums[i].y * (1.0f / D) * inv;
+            const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-mean, -mean);
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                x.a[k] = __fmul2_rn(__fmul2_rn(x.a[k], inv2), gain.a[k]);
-                x.b[k] = __fmul2_rn(__fmul2_rn(x.b[k], inv2), gain.b[k]);
-              }
-            }
-            if (rot) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float2 p = x.a[k], q = x.b[k];
-                x.a[k] = __ffma2_rn(p, cs[k], __fmul2_rn(q, ns[k]));
-                x.b[k] = __ffma2_rn(q, cs[k], __fmul2_rn(p, sn[k]));
-              }
-            }
-            uint2 u, v;
-            pack<T, INTER>(x, u, v);
-            *reinterpret_cast<uint2*>(yp) = u;
-            *reinterpret_cast<uint2*>(yp + dv) = v;
-            yp += ys;
-          }
-        } else {
-          Pairs g[R];
-          float2 sums[R];  // of x^2 and of gx x: xhat = x inv, inv known only after them
-#pragma unroll
-          for (int i = 0; i < R; ++i) {
-            g[i] = unpack<T, INTER>(gu[i], gv[i]);
-            if (rot) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float2 p = g[i].a[k], q = g[i].b[k];
-                g[i].a[k] = __ffma2_rn(p, cs[k], __fmul2_rn(q, sn[k]));
-                g[i].b[k] = __ffma2_rn(q, cs[k], __fmul2_rn(p, ns[k]));
-              }
-            }
-            if (a.norm) {
-              const Pairs x = unpack<T, INTER>(xu[i], xv[i]);
-              float2 ss = make_float2(0.0f, 0.0f), dot = ss;
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                ss = __ffma2_rn(x.a[k], x.a[k], __ffma2_rn(x.b[k], x.b[k], ss));
-                dot = __ffma2_rn(__fmul2_rn(g[i].a[k], gain.a[k]), x.a[k], dot);
-                dot = __ffma2_rn(__fmul2_rn(g[i].b[k], gain.b[k]), x.b[k], dot);
-              }
-              sums[i] = make_float2(ss.x + ss.y, dot.x + dot.y);
+            for (int k = 0; k < 2; ++k) {
+              x.a[k] = __fmul2_rn(x.a[k], inv2);
+              x.b[k] = __fmul2_rn(x.b[k], inv2);
+              dgain.a[k] = __ffma2_rn(g[i].a[k], x.a[k], dgain.a[k]);
+              dgain.b[k] = __ffma2_rn(g[i].b[k], x.b[k], dgain.b[k]);
+              g[i].a[k] = __fmul2_rn(
+                  __ffma2_rn(x.a[k], neg2, __fmul2_rn(g[i].a[k], gain.a[k])), inv2);
+              g[i].b[k] = __fmul2_rn(
+                  __ffma2_rn(x.b[k], neg2, __fmul2_rn(g[i].b[k], gain.b[k])), inv2);
             }
           }
-          if (a.norm) {
-#pragma unroll
-            for (int o = LPR / 2; o >= 1; o >>= 1)
-#pragma unroll
-              for (int i = 0; i < R; ++i)
-                sums[i] = __fadd2_rn(sums[i], make_float2(__shfl_xor_sync(mask, sums[i].x, o),
-                                                          __shfl_xor_sync(mask, sums[i].y, o)));
-          }
-#pragma unroll
-          for (int i = 0; i < R; ++i) {
-            if (a.norm) {
-              Pairs x = unpack<T, INTER>(xu[i], xv[i]);
-              const float inv = rsqrtf(fmaf(sums[i].x, 1.0f / D, a.eps));
-              // xhat mean(gx xhat) = xhat * (mean(gx x) inv)
-              const float mean = sums[i].y * (1.0f / D) * inv;
-              const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-mean, -mean);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                x.a[k] = __fmul2_rn(x.a[k], inv2);
-                x.b[k] = __fmul2_rn(x.b[k], inv2);
-                dgain[w].a[k] = __ffma2_rn(g[i].a[k], x.a[k], dgain[w].a[k]);
-                dgain[w].b[k] = __ffma2_rn(g[i].b[k], x.b[k], dgain[w].b[k]);
-                g[i].a[k] = __fmul2_rn(
-                    __ffma2_rn(x.a[k], neg2, __fmul2_rn(g[i].a[k], gain.a[k])), inv2);
-                g[i].b[k] = __fmul2_rn(
-                    __ffma2_rn(x.b[k], neg2, __fmul2_rn(g[i].b[k], gain.b[k])), inv2);
-              }
-            }
-            uint2 u, v;
-            pack<T, INTER>(g[i], u, v);
-            *reinterpret_cast<uint2*>(yp) = u;
-            *reinterpret_cast<uint2*>(yp + dv) = v;
-            yp += ys;
-          }
+          uint2 u, v;
+          pack<T, INTER>(g[i], u, v);
+          *reinterpret_cast<uint2*>(yp) = u;
+          *reinterpret_cast<uint2*>(yp + dv) = v;
+          yp += ys;
         }
-        h += R;
-      };
-      while (h + UN <= end) rows(std::integral_constant<int, UN>{});
-      while (h < end) rows(std::integral_constant<int, 1>{});
-    }
+      }
+      h += R;
+    };
+    while (h + UN <= hi) rows(std::integral_constant<int, UN>{});
+    while (h < hi) rows(std::integral_constant<int, 1>{});
   }
   if constexpr (BWD) {
     if (a.partial == nullptr) return;
     // the block's sums, groups in order
     __shared__ float red[GROUPS][D];
+    float* row = red[threadIdx.x / LPR];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      __syncthreads();
-      float* row = red[threadIdx.x / LPR];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 p = dgain[w].a[i], q = dgain[w].b[i];
-        if (INTER) {
-          float* at = row + (i == 0 ? cu : cv);
-          at[0] = p.x;
-          at[1] = q.x;
-          at[2] = p.y;
-          at[3] = q.y;
-        } else {
-          row[cu + 2 * i] = p.x;
-          row[cu + 2 * i + 1] = p.y;
-          row[cv + 2 * i] = q.x;
-          row[cv + 2 * i + 1] = q.y;
-        }
+    for (int i = 0; i < 2; ++i) {
+      const float2 p = dgain.a[i], q = dgain.b[i];
+      if (INTER) {
+        float* at = row + (i == 0 ? cu : cv);
+        at[0] = p.x;
+        at[1] = q.x;
+        at[2] = p.y;
+        at[3] = q.y;
+      } else {
+        row[cu + 2 * i] = p.x;
+        row[cu + 2 * i + 1] = p.y;
+        row[cv + 2 * i] = q.x;
+        row[cv + 2 * i + 1] = q.y;
       }
-      __syncthreads();
-      for (int c = threadIdx.x; c < D; c += kThreads) {
-        float sum = 0.0f;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += kThreads) {
+      float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < GROUPS; ++i) sum += red[i][c];
-        a.partial[(static_cast<size_t>(blockIdx.x) * 2 + w) * D + c] = sum;
-      }
+      for (int i = 0; i < GROUPS; ++i) sum += red[i][c];
+      a.partial[static_cast<size_t>(blockIdx.x) * D + c] = sum;
     }
   }
 }
 
-// dgain from the blocks' partial sums: 32 channels per block, 32 threads per channel each
-// sum every 32nd partial, then a tree, all in a fixed order.
+// dgain from the blocks' partial sums (the first blocks_q are q's): 32 channels per block, 32
+// threads per channel each sum every 32nd partial, then a tree, all in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(1024)
-    dgain_kernel(const float* partial, int blocks, float* dgain_q, float* dgain_k) {
+    dgain_kernel(const float* partial, int blocks_q, int blocks, float* dgain_q, float* dgain_k) {
   __shared__ float red[32][33];
   const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + c;  // column of [2][D]
+  const bool on_k = blockIdx.x >= D / 32;
+  const int col = (blockIdx.x % (D / 32)) * 32;
+  const int end = on_k ? blocks : blocks_q;
   float sum = 0.0f;
-  for (int i = r; i < blocks; i += 32) sum += partial[static_cast<size_t>(i) * 2 * D + col];
+  for (int i = (on_k ? blocks_q : 0) + r; i < end; i += 32)
+    sum += partial[static_cast<size_t>(i) * D + col + c];
   red[r][c] = sum;
   __syncthreads();
   // transposed: warp r now holds channel r
   float v = red[c][r];
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (c == 0) {
-    const int out = blockIdx.x * 32 + r;
-    if (out < D) dgain_q[out] = v;
-    else dgain_k[out - D] = v;
-  }
+  if (c == 0) (on_k ? dgain_k : dgain_q)[col + r] = v;
 }
 
 }  // namespace rope

@@ -130,7 +130,7 @@ def _params(q, k, positions, rope: Rope, gains) -> Tuple[SageRopeParams, Optiona
         if (bits == 64 and positions.dtype != torch.int64) or positions.get_device() != dev:
             raise ValueError("positions must be int32 or int64 on q's device")
         ps, axes = tuple(positions.shape), rope.axes
-        if axes == 1 and len(ps) > 1 and ps[0] == 1 and ps != (B, N):
+        if axes == 1 and len(ps) > 1 and ps[0] == 1 and (len(qs) == 3 or ps != (B, N)):
             ps = ps[1:]  # [1, N] or [1, B, N]
         shared, own = ((N,), (B, N)) if axes == 1 else ((axes, N), (axes, B, N))
         if (ps != shared and (len(qs) != 4 or ps != own)) or not positions.is_contiguous():
