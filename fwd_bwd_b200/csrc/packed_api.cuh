@@ -150,7 +150,10 @@ int run_rope(sage::rope::Args* a, float* dgain_q, float* dgain_k, cudaStream_t s
   a->blocks_q = static_cast<int>(std::min<int64_t>(tiles * a->chunks[0], for_q));
   const int blocks =
       a->blocks_q + static_cast<int>(std::min<int64_t>(tiles * a->chunks[1], most - for_q));
-  sage::rope::qk_rope_kernel<T, D, INTER, BWD><<<blocks, sage::rope::kThreads, 0, st>>>(*a);
+  auto kern = sage::rope::qk_rope_kernel<T, D, INTER, BWD>;
+  const size_t smem = BWD ? sage::rope::kBwdSmem : 0;
+  if (BWD && set_smem(kern, smem) != SAGE_OK) return SAGE_ERR_CUDA;
+  kern<<<blocks, sage::rope::kThreads, smem, st>>>(*a);
   if (BWD && a->partial)
     sage::rope::dgain_kernel<D><<<2 * D / 32, 1024, 0, st>>>(a->partial, a->blocks_q, blocks,
                                                                  dgain_q, dgain_k);

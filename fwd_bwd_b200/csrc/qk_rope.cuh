@@ -10,6 +10,9 @@
 // 4 sines and cosines.  Such a group of lanes walks the heads of one token, because the angles
 // depend on the token only, a few rows at a time so that their loads and their row sums overlap.
 // The blocks are split between q and k by their heads (a warp never works on both).
+// The backward reads two rows and keeps more per row in registers, so too few bytes would be in
+// flight; each of its threads copies its own channels kAhead rows ahead into shared memory that
+// only it reads (no barrier: its own copy groups order it).
 //
 // Angles: frequency i as F_i = inv_freq_i / (2 pi) * 2^64 modulo 2^64, so position * F_i
 // modulo 2^64 is the angle's fraction of a turn, with all full turns dropped exactly: the same
@@ -32,6 +35,8 @@ namespace rope {
 
 constexpr int kThreads = 256;
 constexpr int kMaxAxes = 4;
+constexpr int kAhead = 4;  // rows, backward
+constexpr size_t kBwdSmem = static_cast<size_t>(kAhead) * 4 * kThreads * 8;
 
 struct Rows {
   char* ptr;
@@ -111,6 +116,8 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3)
     cv = cu + 4;
   }
   const int dv = cv - cu;
+  extern __shared__ uint2 rope_smem[];  // backward: [kAhead][4][kThreads], then the sums
+  uint2* ring = rope_smem + threadIdx.x;
   Pairs dgain, gain;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -186,19 +193,40 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3)
       fresh = false;
     };
     int h = lo;
+    int slot = 0, next = lo;  // backward: of row h in the ring; next row to copy
+    auto copy = [&](int s) {
+      if (next < hi) {
+        uint2* at_s = ring + s * 4 * kThreads;
+        copy_async8(at_s, xp);
+        copy_async8(at_s + kThreads, xp + dv);
+        copy_async8(at_s + 2 * kThreads, gp);
+        copy_async8(at_s + 3 * kThreads, gp + dv);
+        xp += xs;
+        gp += gs;
+        ++next;
+      }
+      copy_async_commit();  // a group per row, empty ones too: the waits count groups
+    };
+    if (BWD)
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) copy(s);
     // R rows from h on
     auto rows = [&](auto count) {
       constexpr int R = decltype(count)::value;
       uint2 xu[R], xv[R], gu[R], gv[R];
+      if (BWD) copy_async_wait<kAhead - R>();
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        xu[i] = __ldcs(reinterpret_cast<const uint2*>(xp));
-        xv[i] = __ldcs(reinterpret_cast<const uint2*>(xp + dv));
-        xp += xs;
         if (BWD) {
-          gu[i] = __ldcs(reinterpret_cast<const uint2*>(gp));
-          gv[i] = __ldcs(reinterpret_cast<const uint2*>(gp + dv));
-          gp += gs;
+          const uint2* at_s = ring + ((slot + i) % kAhead) * 4 * kThreads;
+          xu[i] = at_s[0];
+          xv[i] = at_s[kThreads];
+          gu[i] = at_s[2 * kThreads];
+          gv[i] = at_s[3 * kThreads];
+        } else {
+          xu[i] = __ldcs(reinterpret_cast<const uint2*>(xp));
+          xv[i] = __ldcs(reinterpret_cast<const uint2*>(xp + dv));
+          xp += xs;
         }
       }
       if (fresh) angles();
@@ -308,14 +336,21 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 3)
         }
       }
       h += R;
+      if (BWD) {  // these rows have been used: their places are free
+#pragma unroll
+        for (int i = 0; i < R; ++i) copy((slot + i) % kAhead);
+        slot = (slot + R) % kAhead;
+      }
     };
     while (h + UN <= hi) rows(std::integral_constant<int, UN>{});
     while (h < hi) rows(std::integral_constant<int, 1>{});
   }
   if constexpr (BWD) {
+    copy_async_wait<0>();
     if (a.partial == nullptr) return;
     // the block's sums, groups in order
-    __shared__ float red[GROUPS][D];
+    __syncthreads();  // every thread has read its rows
+    float(*red)[D] = reinterpret_cast<float(*)[D]>(rope_smem);
     float* row = red[threadIdx.x / LPR];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

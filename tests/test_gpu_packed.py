@@ -324,3 +324,110 @@ def test_only_empty_sequences():
     q, k, v, do = _inputs(5, 2, 1, 64, BF, "plain")
     got = _run(q, k, v, do, [0, 0])
     assert not any(x.any() for x in got.values())
+
+
+@pytest.mark.parametrize("d,heads", [(64, (8, 8)), (64, (9, 3)), (128, (8, 8)), (128, (12, 4))],
+                         ids=str)
+def test_many_tiles_on_a_full_device(d, heads):
+    """More tiles than the device holds at once, many keys per tile: every pipeline's buffers turn
+    over many times while other CTAs share the SMs."""
+    lengths = [2048, 1900, 1337, 700, 640, 511]
+    q, k, v, do = _inputs(sum(lengths), *heads, d, BF, seed=21)
+    for causal in (True, False):
+        _check(_run(q, k, v, do, lengths, causal), q, k, v, do, lengths, causal)
+
+
+def test_repeated_launches_finish():
+    """Back-to-back launches of every kernel on a full device: no bounded wait runs out."""
+    for d in (64, 128):
+        lengths = [1024] * 12
+        q, k, v, do = _inputs(sum(lengths), 16, 8, d, BF, seed=22)
+        b = packed.Batch(lengths)
+        want = None
+        for _ in range(30):
+            o, lse = packed.attn_fwd(q, k, v, b)
+            grads = packed.attn_bwd(q, k, v, o, lse, do, b)
+            if want is None:
+                want = (o, lse, *grads)
+        torch.cuda.synchronize()
+        assert ops.device_status() == 0
+        for x, y in zip(want, (o, lse, *grads)):
+            assert torch.equal(x, y)
+
+
+def test_batch_of_another_layer_and_two_graphs():
+    """One Batch under two captured graphs with workspaces of their own, replayed in turn."""
+    lengths = [260, 90]
+    b = packed.Batch(lengths)
+    sets, graphs = [], []
+    for seed, (hq, hkv, d, dt) in enumerate([(4, 2, 64, HF), (3, 3, 128, BF)]):
+        q, k, v, do = _inputs(sum(lengths), hq, hkv, d, dt, "plain", seed=30 + seed)
+        ws = torch.empty(packed.workspace_bytes(q, k, v, b), dtype=torch.uint8, device="cuda")
+        o, lse = packed.attn_fwd(q, k, v, b)
+        packed.attn_bwd(q, k, v, o, lse, do, b, workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            packed.attn_fwd(q, k, v, b, o=o, lse=lse)
+            grads = packed.attn_bwd(q, k, v, o, lse, do, b, workspace=ws)
+        sets.append((q, k, v, do, o, lse, grads))
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert ops.device_status() == 0
+    for q, k, v, do, o, lse, grads in sets:
+        want = _run(q, k, v, do, lengths)
+        for n, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+            assert torch.equal(x, want[n]), n
+
+
+def test_threads_and_streams_at_once():
+    """Two host threads on streams of their own, each with its own tensors."""
+    import threading
+
+    lengths = [400, 128, 33]
+    b = packed.Batch(lengths)
+    inputs = [_inputs(sum(lengths), 4, 2, 64 * (1 + i % 2), BF, "plain", seed=40 + i)
+              for i in range(2)]
+    want = [_run(*x, lengths) for x in inputs]
+    got, errors = [None, None], []
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                q, k, v, do = inputs[i]
+                for _ in range(5):
+                    o, lse = packed.attn_fwd(q, k, v, b)
+                    grads = packed.attn_bwd(q, k, v, o, lse, do, b)
+                torch.cuda.current_stream().synchronize()
+                got[i] = (o, lse, *grads)
+        except Exception as e:  # noqa: BLE001 - reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert ops.device_status() == 0
+    for i in range(2):
+        for n, x in zip(("o", "lse", "dq", "dk", "dv"), got[i]):
+            assert torch.equal(x, want[i][n]), (i, n)
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("d", [64, 128])
+def test_single_keys_have_no_score_gradient(d, dt):
+    """Sequences of one token: P = 1, so dQ and dK vanish (to float32 rounding of dP) and dV = dO."""
+    lengths = [1] * 50
+    q, k, v, do = _inputs(50, 2, 1, d, dt, "plain", seed=50, do_scale=1.0)
+    got = _run(q, k, v, do, lengths)
+    R.close(got["dv"], R.attention(q, k, v, lengths, True, d ** -0.5, do), "dv")
+    size = (do.double().abs()[:, :, None] * v.double().abs()[:, None]).sum(-1).max()
+    # dS = P dP - P (P dP) with P = exp2 of a rounding error: |dS| <= 2^-18 |dO| |v|
+    for n, other in (("dq", k), ("dk", q)):
+        assert float(got[n].double().abs().max()) <= float(
+            2.0 ** -18 * size * d ** -0.5 * other.double().abs().max() * 2 + R.tiny(dt)), n
