@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <new>
 #include <vector>
 
@@ -45,7 +46,7 @@ int check_rope(const sage_rope_params* p) {
   if (!p || p->B <= 0 || p->N <= 0 || p->Hq <= 0 || p->Hkv <= 0) return SAGE_ERR_INVALID_ARG;
   if (p->dtype != SAGE_FP16 && p->dtype != SAGE_BF16) return SAGE_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return SAGE_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(p->B) * p->N >= (int64_t{1} << 31) || p->Hq > 65536 ||
+  if (static_cast<int64_t>(p->B) * p->N >= (int64_t{1} << 31) - 64 || p->Hq > 65536 ||
       p->Hkv > 65536)
     return SAGE_ERR_UNSUPPORTED;
   if ((p->norm != 0 && p->norm != 1) || (p->interleaved != 0 && p->interleaved != 1))
@@ -227,7 +228,9 @@ int check_packed(const sage_packed_params* p, const sage_packed_info* info, cons
   if (info->sequences < 1 || info->tiles < 0 || info->pairs < 0 || info->pairs > info->tiles ||
       info->tokens < 0 || info->tokens > p->T)
     return SAGE_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(info->tiles) * p->Hq >= (int64_t{1} << 31)) return SAGE_ERR_UNSUPPORTED;
+  // CTAs of the row pass, the largest grid
+  if (static_cast<int64_t>(info->tiles) * (p->Hq + p->Hkv) >= (int64_t{1} << 31))
+    return SAGE_ERR_UNSUPPORTED;
   if (!aligned16(plan)) return SAGE_ERR_ALIGNMENT;
   return SAGE_OK;
 }
@@ -270,14 +273,18 @@ sage::packed::Out packed_out(const sage_rows* r) {
   return {static_cast<char*>(r->ptr), r->token_stride, r->head_stride};
 }
 
-template <typename K, typename... A>
-int launch_packed(K kern, int regs, int64_t grid, int threads, size_t smem, cudaStream_t st,
-                  const A&... args) {
-  if (set_smem(kern, smem) != SAGE_OK) return SAGE_ERR_CUDA;
-  // kernels that move registers between warpgroups (setmaxnreg): the split is sized for exactly
-  // this launch allocation
-  if (regs != 0 && launch_regs(kern) != regs) return SAGE_ERR_UNSUPPORTED;
-  kern<<<static_cast<unsigned>(grid), threads, smem, st>>>(args...);
+// REGS: the launch allocation that the kernel's register split (setmaxnreg) is sized for; 0: none.
+template <auto KERN, int REGS, typename... A>
+int launch_packed(int64_t grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  if (set_smem(KERN, smem) != SAGE_OK) return SAGE_ERR_CUDA;
+  if (REGS != 0) {
+    // a property of the compiled kernel: asked for once
+    static std::atomic<int> regs{0};
+    int r = regs.load(std::memory_order_relaxed);
+    if (r <= 0) regs.store(r = launch_regs(KERN), std::memory_order_relaxed);
+    if (r != REGS) return SAGE_ERR_UNSUPPORTED;
+  }
+  KERN<<<static_cast<unsigned>(grid), threads, smem, st>>>(args...);
   return launch_status();
 }
 
@@ -320,19 +327,19 @@ int run_packed_fwd(const sage_packed_params* p, const sage_packed_info* info, co
   if constexpr (D == 64) {
     a.grid = {plan_list(plan, info, p->causal, false), info->tiles, p->Hq,
               grid_chunk(p, info, p->Hq, kv_bytes / a.group)};
-    return launch_packed(F::attn_fwd64_kernel<T>, 0,
-                         static_cast<int64_t>(info->tiles) * p->Hq, F::kThreads64,
-                         F::smem64_bytes<T>(), st, tq, tk, tv, a);
+    return launch_packed<F::attn_fwd64_kernel<T>, 0>(static_cast<int64_t>(info->tiles) * p->Hq,
+                                                     F::kThreads64, F::smem64_bytes<T>(), st, tq,
+                                                     tk, tv, a);
   } else {
     const bool heads = a.group % 2 == 0;
     const int ctas = heads ? p->Hq / 2 : p->Hq;  // per item
     a.grid = {plan_list(plan, info, p->causal, !heads), heads ? info->tiles : info->pairs, ctas,
               grid_chunk(p, info, ctas, kv_bytes / (heads ? a.group / 2 : a.group))};
     const int64_t grid = static_cast<int64_t>(a.grid.n_items) * ctas;
-    return heads ? launch_packed(F::attn_fwd_kernel<T, D, true>, F::kLaunchRegs, grid, F::kThreads,
-                                 F::smem_bytes<T, D>(), st, tq, tk, tv, a)
-                 : launch_packed(F::attn_fwd_kernel<T, D, false>, F::kLaunchRegs, grid,
-                                 F::kThreads, F::smem_bytes<T, D>(), st, tq, tk, tv, a);
+    return heads ? launch_packed<F::attn_fwd_kernel<T, D, true>, F::kLaunchRegs>(
+                       grid, F::kThreads, F::smem_bytes<T, D>(), st, tq, tk, tv, a)
+                 : launch_packed<F::attn_fwd_kernel<T, D, false>, F::kLaunchRegs>(
+                       grid, F::kThreads, F::smem_bytes<T, D>(), st, tq, tk, tv, a);
   }
 }
 
@@ -394,15 +401,16 @@ int run_packed_bwd(const sage_packed_params* p, const sage_packed_info* info, co
   // dq_kernel first: it refines D for dkv_kernel
   a.grid = {r.items, info->tiles, p->Hq, grid_chunk(p, info, p->Hq, pair_bytes / r.group)};
   a.out[0] = packed_out(dq);
-  s = launch_packed(B::dq_kernel<T, D>, B::Cfg<D>::kLaunchRegs, static_cast<int64_t>(info->tiles) * p->Hq,
-                    B::Cfg<D>::kThreads, B::dq_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
+  s = launch_packed<B::dq_kernel<T, D>, B::Cfg<D>::kLaunchRegs>(
+      static_cast<int64_t>(info->tiles) * p->Hq, B::Cfg<D>::kThreads, B::dq_smem_bytes<T, D>(), st,
+      tq, tk, tv, tdo, a);
   if (s != SAGE_OK) return s;
   a.grid = {r.items, info->tiles, p->Hkv, grid_chunk(p, info, p->Hkv, pair_bytes * r.group)};
   a.out[0] = packed_out(dv);
   a.out[1] = packed_out(dk);
-  return launch_packed(B::dkv_kernel<T, D>, B::Cfg<D>::kLaunchRegs,
-                       static_cast<int64_t>(info->tiles) * p->Hkv, B::Cfg<D>::kThreads,
-                       B::dkv_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
+  return launch_packed<B::dkv_kernel<T, D>, B::Cfg<D>::kLaunchRegs>(
+      static_cast<int64_t>(info->tiles) * p->Hkv, B::Cfg<D>::kThreads, B::dkv_smem_bytes<T, D>(),
+      st, tq, tk, tv, tdo, a);
 }
 
 }  // namespace

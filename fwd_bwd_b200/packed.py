@@ -46,7 +46,18 @@ class Batch:
             arr, len(self.lengths), host.data_ptr(), n, ctypes.byref(self.info)))
         self.plan = host.to(torch.device(device))
         self.plan_ptr = self.plan.data_ptr()
+        self._stream = 0
+        if self.plan.is_cuda:
+            # complete before any stream reads it
+            stream = torch.cuda.current_stream(self.plan.device)
+            stream.synchronize()
+            self._stream = stream.cuda_stream
         self.tokens = int(self.info.tokens)
+
+    def _used_on(self, stream: torch.cuda.Stream) -> None:
+        """Keeps the plan's memory from its allocating stream while another one reads it."""
+        if stream.cuda_stream != self._stream:
+            self.plan.record_stream(stream)
 
     @property
     def device(self) -> torch.device:
@@ -76,7 +87,7 @@ def _params(q, k, v, batch: Batch, causal: bool, softmax_scale: float) -> SagePa
 
 def _new(like: torch.Tensor, batch: Batch) -> torch.Tensor:
     """An output for ``like``'s shape whose rows behind the last sequence are zero."""
-    x = like.new_empty(like.shape)
+    x = torch.empty_like(like, memory_format=torch.contiguous_format)
     if like.shape[0] > batch.tokens:
         x[batch.tokens:].zero_()
     return x
@@ -113,7 +124,7 @@ def attn_fwd(q, k, v, batch: Batch, causal: bool = True, softmax_scale: float = 
         _check_lse(lse, q)
     rows_o = _like("o", o, q)
     if batch.tokens:
-        _call("sage_packed_attn_fwd", q.get_device(), prm, batch.info, batch.plan_ptr, _rows(q),
+        _call("sage_packed_attn_fwd", q.get_device(), batch._used_on, prm, batch.info, batch.plan_ptr, _rows(q),
               _rows(k), _rows(v), rows_o, lse.data_ptr())
     return o, lse
 
@@ -140,7 +151,7 @@ def attn_bwd(q, k, v, o, lse, dout, batch: Batch, causal: bool = True, softmax_s
         workspace = torch.empty(_workspace_bytes(prm, batch), dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != q.get_device() or not workspace.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on q's device")
-    _call("sage_packed_attn_bwd", q.get_device(), prm, batch.info, batch.plan_ptr, *rows,
+    _call("sage_packed_attn_bwd", q.get_device(), batch._used_on, prm, batch.info, batch.plan_ptr, *rows,
           lse.data_ptr(), rows_do, *grads, workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
     return dq, dk, dv

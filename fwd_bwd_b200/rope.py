@@ -83,6 +83,10 @@ def _rows(x: torch.Tensor) -> SageRows:
     return SageRows(x.data_ptr(), s[0], s[2], s[1])
 
 
+def _new(like: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
+
+
 def _like(name: str, x: torch.Tensor, like: torch.Tensor) -> SageRows:
     """``_rows`` of a tensor that belongs to ``like``."""
     if x.shape != like.shape or x.dtype != like.dtype or x.get_device() != like.get_device():
@@ -149,9 +153,13 @@ def _ptr(x: Optional[torch.Tensor]) -> Optional[int]:
     return None if x is None else x.data_ptr()
 
 
-def _call(name: str, device: int, *args) -> None:
-    """Calls the library on the tensors' device and its current stream."""
-    stream = torch.cuda.current_stream(device).cuda_stream
+def _call(name: str, device: int, used_on, *args) -> None:
+    """Calls the library on the tensors' device and its current stream, of which ``used_on`` (or
+    None) is told."""
+    stream = torch.cuda.current_stream(device)
+    if used_on is not None:
+        used_on(stream)
+    stream = stream.cuda_stream
     if torch.cuda.current_device() == device:
         status = getattr(lib(), name)(*args, stream)
     else:
@@ -171,11 +179,11 @@ def qk_norm_rope_fwd(q, k, positions, rope: Rope, gain_q=None, gain_k=None, q_ou
     the caller must not overlap the inputs.
     """
     prm, pos = _params(q, k, positions, rope, (gain_q, gain_k))
-    q_out = q.new_empty(q.shape) if q_out is None else q_out
-    k_out = k.new_empty(k.shape) if k_out is None else k_out
+    q_out = _new(q) if q_out is None else q_out
+    k_out = _new(k) if k_out is None else k_out
     rows_q, rows_k = _like("q_out", q_out, q), _like("k_out", k_out, k)
     if q.numel():
-        _call("sage_qk_norm_rope_fwd", q.get_device(), prm, _rows(q), _rows(k), _ptr(gain_q),
+        _call("sage_qk_norm_rope_fwd", q.get_device(), None, prm, _rows(q), _rows(k), _ptr(gain_q),
               _ptr(gain_k), pos, rows_q, rows_k)
     return q_out, k_out
 
@@ -187,8 +195,8 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, rope: Rope, gain_q=None, g
     The gains' gradients are float32 [d] whether or not gains were given (None without norm).
     """
     prm, pos = _params(q, k, positions, rope, (gain_q, gain_k))
-    dq = q.new_empty(q.shape) if dq is None else dq
-    dk = k.new_empty(k.shape) if dk is None else dk
+    dq = _new(q) if dq is None else dq
+    dk = _new(k) if dk is None else dk
     rows = (_like("dq_out", dq_out, q), _like("dk_out", dk_out, k), _like("dq", dq, q),
             _like("dk", dk, k))
     dgain_q = dgain_k = None
@@ -205,7 +213,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, rope: Rope, gain_q=None, g
     elif workspace is not None and (workspace.get_device() != q.get_device()
                                     or not workspace.is_contiguous()):
         raise ValueError("the workspace must be a contiguous tensor on q's device")
-    _call("sage_qk_norm_rope_bwd", q.get_device(), prm, _rows(q), _rows(k), _ptr(gain_q),
+    _call("sage_qk_norm_rope_bwd", q.get_device(), None, prm, _rows(q), _rows(k), _ptr(gain_q),
           _ptr(gain_k), pos, *rows, _ptr(dgain_q), _ptr(dgain_k), _ptr(workspace),
           0 if workspace is None else workspace.numel() * workspace.element_size())
     return dq, dk, dgain_q, dgain_k

@@ -431,3 +431,26 @@ def test_single_keys_have_no_score_gradient(d, dt):
     for n, other in (("dq", k), ("dk", q)):
         assert float(got[n].double().abs().max()) <= float(
             2.0 ** -18 * size * d ** -0.5 * other.double().abs().max() * 2 + R.tiny(dt)), n
+
+
+def test_batch_freed_while_another_stream_reads_it():
+    """A plan made on one stream, read on another, and dropped at once: its memory is not given to
+    new tensors of the first stream while the kernels run."""
+    lengths = [1024] * 8
+    q, k, v, do = _inputs(sum(lengths), 8, 2, 128, BF, "plain", seed=60)
+    want = _run(q, k, v, do, lengths)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            b = packed.Batch(lengths)
+        o, lse = packed.attn_fwd(q, k, v, b)
+        grads = packed.attn_bwd(q, k, v, o, lse, do, b)
+        size = b.plan.numel()
+        del b
+        with torch.cuda.stream(side):
+            junk = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        assert ops.device_status() == 0 and junk
+        for n, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+            assert torch.equal(x, want[n]), n
