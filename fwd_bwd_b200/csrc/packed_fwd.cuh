@@ -34,9 +34,18 @@
 // a row's maximum grows by more than 2^8: P then stays below 256, exact in the final division
 // by the row sum, and most key tiles leave O untouched.
 // Rounding: P to the tensors' type for P V (the sum l uses the unrounded P); O once at the end.
-// The exponentials all go to the special-function unit: moving an eighth or a quarter of them to
-// the FMA pipe costs more instructions than it frees time (16 heads of 128, 4 x 8192 tokens:
-// 899 us, 921 us and 953 us).
+// A quarter of the exponentials runs on the FMA pipe (32 heads of 128, prompts of 4099 to 8 tokens:
+// 222 us, 224 us with an eighth, 225 us with none; d = 64, images: 38 us against 39 us).
+//
+// Measured (B200, kernel time; causal, 2 products counted over the visible scores):
+//   d = 128, 16384 tokens, 32 / 8 heads, bf16                1643 us, 1338 TFLOP/s
+//   d = 128, 4 x 8192, 16 heads                               868 us, 1267 TFLOP/s
+//   d = 64, 8 x 2048, 16 heads                                112 us,  614 TFLOP/s
+// (cuBLAS bf16: 1614 TFLOP/s for a moment, 1368 under the power cap, which the first two reach
+// after some milliseconds: 1896 us in a loop.)  Bound: d = 128 by the chain S -> softmax -> P V of
+// two tiles that take turns (tensor pipe 56% active, special-function unit 56%); d = 64 by the
+// exponentials and the instructions around them (special-function unit 60%, tensor pipe 30%), with
+// a fixed 28 us for setting up and storing 2048 CTAs, partly hidden by the four to an SM.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -190,6 +199,9 @@ __device__ __forceinline__ float2 exp2_fma2(float2 z) {
   return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
                      __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
 }
+
+// Pairs whose exponentials run on the FMA pipe.
+__device__ __forceinline__ constexpr bool poly_pair(int i) { return (i & 3) == 3; }
 
 namespace fwd {
 
@@ -430,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          z[k] = make_float2(ex2_approx(z[k].x), ex2_approx(z[k].y));
+          z[k] = !MASK && poly_pair(k) ? exp2_fma2(z[k])
+                                       : make_float2(ex2_approx(z[k].x), ex2_approx(z[k].y));
         uint32_t w[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
@@ -660,7 +673,8 @@ __global__ void __launch_bounds__(kThreads64, 4)
         for (int k = 0; k < 16; ++k) {
           const float2 z = __ffma2_rn(
               make_float2(__uint_as_float(x[q][2 * k]), __uint_as_float(x[q][2 * k + 1])), c2, n2);
-          const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+          const float2 p = !MASK && poly_pair(k) ? exp2_fma2(z)
+                                                 : make_float2(ex2_approx(z.x), ex2_approx(z.y));
           if (k & 1)
             sum2 = __fadd2_rn(sum2, p);
           else
