@@ -155,7 +155,9 @@ def lib() -> ctypes.CDLL:
         L.sage_packed_plan_bytes.restype = sz
         L.sage_packed_plan_fill.argtypes = [P(ctypes.c_int), i, vp, sz, PI]
         L.sage_packed_plan_fill.restype = i
-        L.sage_packed_attn_fwd.argtypes = [PP, PI, vp, R, R, R, R, vp, vp]
+        L.sage_packed_attn_fwd_workspace_bytes.argtypes = [PP, PI]
+        L.sage_packed_attn_fwd_workspace_bytes.restype = sz
+        L.sage_packed_attn_fwd.argtypes = [PP, PI, vp, R, R, R, R, vp, vp, sz, vp]
         L.sage_packed_attn_fwd.restype = i
         L.sage_packed_attn_bwd_workspace_bytes.argtypes = [PP, PI]
         L.sage_packed_attn_bwd_workspace_bytes.restype = sz

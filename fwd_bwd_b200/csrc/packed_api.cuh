@@ -228,8 +228,9 @@ int check_packed(const sage_packed_params* p, const sage_packed_info* info, cons
   if (info->sequences < 1 || info->tiles < 0 || info->pairs < 0 || info->pairs > info->tiles ||
       info->tokens < 0 || info->tokens > p->T)
     return SAGE_ERR_INVALID_ARG;
-  // CTAs of the row pass, the largest grid
-  if (static_cast<int64_t>(info->tiles) * (p->Hq + p->Hkv) >= (int64_t{1} << 31))
+  // CTAs of the largest grids
+  if (static_cast<int64_t>(info->tiles) * 8 * (static_cast<int64_t>(p->Hq) + p->Hkv) >=
+      (int64_t{1} << 31))
     return SAGE_ERR_UNSUPPORTED;
   if (!aligned16(plan)) return SAGE_ERR_ALIGNMENT;
   return SAGE_OK;
@@ -309,10 +310,58 @@ int grid_chunk(const sage_packed_params* p, const sage_packed_info* info, int he
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(heads, std::max(fit, busy))));
 }
 
+// Parts that a kernel's walks are cut into.  A CTA walks all the tiles its own tile meets; with few
+// heads that leaves SMs idle or one long walk at the end.  Cut when the longest walk (steps) is
+// twice the device's share of all of them or more, into parts of eight steps at least, eight parts
+// at most (each costs 8 bytes of traffic per element of the output, and the joining kernel some 4 us;
+// 2048 tokens, 32 query heads on one key head of 128: dK/dV 621 -> 95 + 4 us; 8192 tokens, one
+// head: 89 -> 51 + 7 us, forward 99 -> 34 us; where the longest walk is 1.1 times the share, 32 heads
+// on one, cutting costs: forward 43 -> 69 us).
+int walk_splits(int64_t longest, int64_t all, int places) {
+  const int64_t share = std::max<int64_t>(1, all / places);
+  return static_cast<int>(std::max<int64_t>(
+      1, std::min<int64_t>({longest / share, longest / 8, 8})));
+}
+int64_t all_steps(const sage_packed_params* p, const sage_packed_info* info) {
+  return (p->causal ? info->causal_steps : info->full_steps) * p->Hq;
+}
+int64_t longest_tiles(const sage_packed_info* info) {
+  return (static_cast<int64_t>(info->longest) + 127) / 128;
+}
+// Forward: d = 128 takes two tiles per CTA, d = 64 four CTAs per SM, the backward two.
+int fwd_splits(const sage_packed_params* p, const sage_packed_info* info) {
+  const bool wide = p->d == 128;
+  return walk_splits(longest_tiles(info), all_steps(p, info) / (wide ? 2 : 1),
+                     148 * (wide ? 1 : 4));
+}
+int dq_splits(const sage_packed_params* p, const sage_packed_info* info) {
+  return walk_splits(longest_tiles(info), all_steps(p, info),
+                     148 * (p->d == 64 ? 2 : 1));
+}
+int dkv_splits(const sage_packed_params* p, const sage_packed_info* info) {
+  return walk_splits(longest_tiles(info) * (p->Hq / p->Hkv), all_steps(p, info),
+                     148 * (p->d == 64 ? 2 : 1));
+}
+
+// Forward workspace, with parts: O [splits][tokens][Hq][d], then maxima and sums.
+struct FwdWs {
+  int splits;
+  size_t stats, total;
+};
+FwdWs fwd_ws(const sage_packed_params* p, const sage_packed_info* info) {
+  FwdWs w = {fwd_splits(p, info), 0, 0};
+  if (w.splits > 1) {
+    const size_t rows = static_cast<size_t>(w.splits) * info->tokens * p->Hq;
+    w.stats = align_up(rows * p->d * 4);
+    w.total = align_up(w.stats + rows * 8);
+  }
+  return w;
+}
+
 template <typename T, int D>
 int run_packed_fwd(const sage_packed_params* p, const sage_packed_info* info, const void* plan,
                    const sage_rows* q, const sage_rows* k, const sage_rows* v, const sage_rows* o,
-                   float* lse, cudaStream_t st) {
+                   float* lse, void* ws, cudaStream_t st) {
   namespace F = sage::packed::fwd;
   CUtensorMap tq, tk, tv;
   if (!make_tile_map(&tq, q, p, p->Hq) || !make_tile_map(&tk, k, p, p->Hkv) ||
@@ -325,36 +374,57 @@ int run_packed_fwd(const sage_packed_params* p, const sage_packed_info* info, co
   a.T = p->T;
   a.causal = p->causal;
   a.scale_log2 = packed_tau(p) * 1.4426950408889634f;
+  const FwdWs w = fwd_ws(p, info);
+  a.splits = w.splits;
+  a.heads = p->Hq;
+  a.part = static_cast<float*>(ws);
+  a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + w.stats);
+  a.tokens = info->tokens;
   const int64_t kv_bytes = info->tokens * D * 2 * 2;
+  int s;
   if constexpr (D == 64) {
-    a.grid = {plan_list(plan, info, p->causal, false), info->tiles, p->Hq,
-              grid_chunk(p, info, p->Hq, kv_bytes / a.group)};
-    return launch_packed<F::attn_fwd64_kernel<T>, 0>(static_cast<int64_t>(info->tiles) * p->Hq,
-                                                     F::kThreads64, F::smem64_bytes<T>(), st, tq,
-                                                     tk, tv, a);
+    const int ctas = p->Hq * w.splits;  // per item
+    a.grid = {plan_list(plan, info, p->causal, false), info->tiles, ctas,
+              grid_chunk(p, info, ctas, kv_bytes / a.group / w.splits)};
+    s = launch_packed<F::attn_fwd64_kernel<T>, 0>(static_cast<int64_t>(info->tiles) * ctas,
+                                                  F::kThreads64, F::smem64_bytes<T>(), st, tq, tk,
+                                                  tv, a);
   } else {
     const bool heads = a.group % 2 == 0;
-    const int ctas = heads ? p->Hq / 2 : p->Hq;  // per item
+    const int ctas = (heads ? p->Hq / 2 : p->Hq) * w.splits;  // per item
     a.grid = {plan_list(plan, info, p->causal, !heads), heads ? info->tiles : info->pairs, ctas,
-              grid_chunk(p, info, ctas, kv_bytes / (heads ? a.group / 2 : a.group))};
+              grid_chunk(p, info, ctas, kv_bytes / (heads ? a.group / 2 : a.group) / w.splits)};
     const int64_t grid = static_cast<int64_t>(a.grid.n_items) * ctas;
-    return heads ? launch_packed<F::attn_fwd_kernel<T, D, true>, F::kLaunchRegs>(
-                       grid, F::kThreads, F::smem_bytes<T, D>(), st, tq, tk, tv, a)
-                 : launch_packed<F::attn_fwd_kernel<T, D, false>, F::kLaunchRegs>(
-                       grid, F::kThreads, F::smem_bytes<T, D>(), st, tq, tk, tv, a);
+    s = heads ? launch_packed<F::attn_fwd_kernel<T, D, true>, F::kLaunchRegs>(
+                    grid, F::kThreads, F::smem_bytes<T, D>(), st, tq, tk, tv, a)
+              : launch_packed<F::attn_fwd_kernel<T, D, false>, F::kLaunchRegs>(
+                    grid, F::kThreads, F::smem_bytes<T, D>(), st, tq, tk, tv, a);
   }
+  if (s != SAGE_OK || w.splits == 1) return s;
+  const int64_t vectors = info->tokens * p->Hq * (D / 8);
+  F::merge_kernel<T, D><<<static_cast<unsigned>((vectors + 255) / 256), 256, 0, st>>>(a);
+  return launch_status();
 }
 
-// Workspace: D [Hq][T]; in half precision also the norms [sequences][Hkv][2].
+// Workspace: D [Hq][T]; in half precision the norms [sequences][Hkv][2]; the parts of dQ, then (in
+// their place) those of dV and dK.
 struct PackedWs {
-  size_t norms, norms_bytes, total;
+  int dq_splits, dkv_splits;
+  size_t norms, norms_bytes, part, total;
 };
 PackedWs packed_ws(const sage_packed_params* p, const sage_packed_info* info) {
   PackedWs w;
   w.norms = align_up(static_cast<size_t>(p->Hq) * p->T * 4);
   w.norms_bytes =
       p->dtype == SAGE_FP16 ? static_cast<size_t>(info->sequences) * p->Hkv * 2 * 4 : 0;
-  w.total = align_up(w.norms + w.norms_bytes);
+  w.part = align_up(w.norms + w.norms_bytes);
+  w.dq_splits = dq_splits(p, info);
+  w.dkv_splits = dkv_splits(p, info);
+  const size_t row = static_cast<size_t>(info->tokens) * p->d * 4;
+  w.total = align_up(
+      w.part + row * std::max(w.dq_splits > 1 ? static_cast<size_t>(w.dq_splits) * p->Hq : 0,
+                              w.dkv_splits > 1 ? static_cast<size_t>(w.dkv_splits) * 2 * p->Hkv
+                                               : 0));
   return w;
 }
 
@@ -396,23 +466,41 @@ int run_packed_bwd(const sage_packed_params* p, const sage_packed_info* info, co
   a.norms = r.norms;
   a.T = p->T;
   a.group = r.group;
+  a.kv_heads = p->Hkv;
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part);
+  a.tokens = info->tokens;
   a.causal = p->causal;
   a.tau = packed_tau(p);
   a.scale_log2 = a.tau * 1.4426950408889634f;
   const int64_t pair_bytes = info->tokens * D * 2 * 2;  // two tensors of one head
+  auto join = [&](int heads, int count) {
+    B::JoinArgs j = {a.part, {a.out[0], a.out[1]}, info->tokens, heads, a.splits, count};
+    const int64_t vectors = count * info->tokens * heads * (D / 8);
+    B::join_kernel<T, D><<<static_cast<unsigned>((vectors + 255) / 256), 256, 0, st>>>(j);
+    return launch_status();
+  };
   // dq_kernel first: it refines D for dkv_kernel
-  a.grid = {r.items, info->tiles, p->Hq, grid_chunk(p, info, p->Hq, pair_bytes / r.group)};
-  a.out[0] = packed_out(dq);
+  a.splits = w.dq_splits;
+  int heads = p->Hq * a.splits;
+  a.grid = {r.items, info->tiles, heads,
+            grid_chunk(p, info, heads, pair_bytes / r.group / a.splits)};
+  a.out[0] = a.out[1] = packed_out(dq);
   s = launch_packed<B::dq_kernel<T, D>, B::Cfg<D>::kLaunchRegs>(
-      static_cast<int64_t>(info->tiles) * p->Hq, B::Cfg<D>::kThreads, B::dq_smem_bytes<T, D>(), st,
+      static_cast<int64_t>(info->tiles) * heads, B::Cfg<D>::kThreads, B::dq_smem_bytes<T, D>(), st,
       tq, tk, tv, tdo, a);
+  if (s == SAGE_OK && a.splits > 1) s = join(p->Hq, 1);
   if (s != SAGE_OK) return s;
-  a.grid = {r.items, info->tiles, p->Hkv, grid_chunk(p, info, p->Hkv, pair_bytes * r.group)};
+  a.splits = w.dkv_splits;
+  heads = p->Hkv * a.splits;
+  a.grid = {r.items, info->tiles, heads,
+            grid_chunk(p, info, heads, pair_bytes * r.group / a.splits)};
   a.out[0] = packed_out(dv);
   a.out[1] = packed_out(dk);
-  return launch_packed<B::dkv_kernel<T, D>, B::Cfg<D>::kLaunchRegs>(
-      static_cast<int64_t>(info->tiles) * p->Hkv, B::Cfg<D>::kThreads, B::dkv_smem_bytes<T, D>(),
-      st, tq, tk, tv, tdo, a);
+  s = launch_packed<B::dkv_kernel<T, D>, B::Cfg<D>::kLaunchRegs>(
+      static_cast<int64_t>(info->tiles) * heads, B::Cfg<D>::kThreads, B::dkv_smem_bytes<T, D>(), st,
+      tq, tk, tv, tdo, a);
+  if (s == SAGE_OK && a.splits > 1) s = join(p->Hkv, 2);
+  return s;
 }
 
 }  // namespace
@@ -512,9 +600,17 @@ int sage_packed_plan_fill(const int* lengths, int sequences, void* host_plan, si
   return SAGE_OK;
 }
 
+size_t sage_packed_attn_fwd_workspace_bytes(const sage_packed_params* p,
+                                            const sage_packed_info* info) {
+  alignas(16) static const char some[16] = {};
+  if (check_packed(p, info, some) != SAGE_OK) return 0;
+  return fwd_ws(p, info).total;
+}
+
 int sage_packed_attn_fwd(const sage_packed_params* p, const sage_packed_info* info,
                          const void* plan, const sage_rows* q, const sage_rows* k,
-                         const sage_rows* v, const sage_rows* o, float* lse, void* stream) {
+                         const sage_rows* v, const sage_rows* o, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
   int s = check_packed(p, info, plan);
   if (s != SAGE_OK) return s;
   const sage_rows* rows[4] = {q, k, v, o};
@@ -524,13 +620,16 @@ int sage_packed_attn_fwd(const sage_packed_params* p, const sage_packed_info* in
       return s;
   if (!lse) return SAGE_ERR_INVALID_ARG;
   if (info->tiles == 0) return SAGE_OK;  // only empty sequences: nothing to write
+  const size_t need = fwd_ws(p, info).total;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SAGE_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return SAGE_ERR_ALIGNMENT;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = p->dtype == SAGE_BF16;
   if (p->d == 128)
-    return bf ? run_packed_fwd<__nv_bfloat16, 128>(p, info, plan, q, k, v, o, lse, st)
-              : run_packed_fwd<__half, 128>(p, info, plan, q, k, v, o, lse, st);
-  return bf ? run_packed_fwd<__nv_bfloat16, 64>(p, info, plan, q, k, v, o, lse, st)
-            : run_packed_fwd<__half, 64>(p, info, plan, q, k, v, o, lse, st);
+    return bf ? run_packed_fwd<__nv_bfloat16, 128>(p, info, plan, q, k, v, o, lse, workspace, st)
+              : run_packed_fwd<__half, 128>(p, info, plan, q, k, v, o, lse, workspace, st);
+  return bf ? run_packed_fwd<__nv_bfloat16, 64>(p, info, plan, q, k, v, o, lse, workspace, st)
+            : run_packed_fwd<__half, 64>(p, info, plan, q, k, v, o, lse, workspace, st);
 }
 
 size_t sage_packed_attn_bwd_workspace_bytes(const sage_packed_params* p,

@@ -171,9 +171,14 @@ struct Args {
   const uint32_t* norms;
   Out out[2];         // dq_kernel: dq; dkv_kernel: dv, dk
   int64_t T;
-  int group;
+  int group, kv_heads;
   int causal;
   float scale_log2, tau;
+  // A CTA's walk may be cut into `splits` parts: the grid then has splits x heads, and the parts go
+  // to part, [splits][tokens][query heads][D] (dq_kernel) or [splits][2 (dV, dK)][tokens][kv_heads][D]
+  int splits;
+  float* part;
+  int64_t tokens;
 };
 
 // P (times 2^shift) of 32 columns from the scores x, in place: z = x c + offset(e).
@@ -210,6 +215,24 @@ __device__ __forceinline__ void pack32(const uint32_t (&x)[32], uint32_t (&w)[16
 // Two neighbouring values of a shared-memory vector, four of which are loaded together.
 __device__ __forceinline__ float2 pair_of(const float4& v, int e) {
   return (e & 2) ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
+}
+
+// 32 sums of a row, scaled, to the output or, in float32, to a part (zeros for one without steps).
+template <typename T>
+__device__ __forceinline__ void store32(const uint32_t (&y)[32], bool any, float scale, T* dst,
+                                        float* part) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8) {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = any ? __uint_as_float(y[e + k]) * scale : 0.0f;
+    if (part == nullptr) {
+      *reinterpret_cast<uint4*>(dst + e) = pack8<T>(f);
+    } else {
+      *reinterpret_cast<float4*>(part + e) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(part + e + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    }
+  }
 }
 
 // ---- dK and dV ------------------------------------------------------------------------------
@@ -249,8 +272,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   // 64 h of their block, over columns that only the same warps have read.
   constexpr uint32_t kColDP = BN, kColDV = 2 * BN, kColDK = 2 * BN + D;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int kv_head;
-  const Item it = grid_at(a.grid, kv_head);
+  int grid_head;
+  const Item it = grid_at(a.grid, grid_head);
+  const int kv_head = grid_head / a.splits, split = grid_head - kv_head * a.splits;
   const int tiles = tiles_of(it);
   // under a causal mask the list's order (most work first) is by query tile: mirrored for keys
   const int kt = a.causal ? tiles - 1 - it.tile : it.tile;
@@ -258,7 +282,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   // first run of query rows that sees these keys and is not all padding
   const int diag = kt * (BT / BN);
   const int first = max(a.causal ? diag : 0, pad / BN);
-  const int n_all = (runs - first) * a.group;
+  // this part's steps of the walk over every head's runs
+  const int walk = (runs - first) * a.group;
+  const int n_from = static_cast<int>(static_cast<int64_t>(walk) * split / a.splits);
+  const int n_all =
+      static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / a.splits) - n_from;
   // the steps' (query head, run of query rows), in order
   struct Walk {
     int head, run, first, runs;
@@ -269,7 +297,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
     }
   };
-  const Walk begin = {kv_head * a.group, first, first, runs};
+  const Walk begin = {kv_head * a.group + n_from / (runs - first), first + n_from % (runs - first),
+                      first, runs};
 
   if (threadIdx.x == 0) {
     sm.abort = device_aborted() ? 1 : 0;
@@ -304,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   if (warp >= C::kProducerWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
     if (warp == C::kProducerWarp) {
-      if (lane == 0) {
+      if (lane == 0 && n_all > 0) {
         mbar_arrive_expect_tx(&sm.kv_full, 2 * BT * D * 2);
         load_tile<T, D, BN, BT>(sm.k, &tm_k, it, kt, kv_head, &sm.kv_full);
         load_tile<T, D, BN, BT>(sm.v, &tm_v, it, kt, kv_head, &sm.kv_full);
@@ -339,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
-      {
+      if (n_all > 0) {
         const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
@@ -400,7 +429,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     const float c = a.scale_log2;
     float factor = 1.0f;  // dS's factor over P's
     if (Scaling<T>::kOn)
-      factor = ds_factor(a.norms + (static_cast<int64_t>(it.seq) * a.grid.heads + kv_head) * 2);
+      factor = ds_factor(a.norms + (static_cast<int64_t>(it.seq) * a.kv_heads + kv_head) * 2);
     const float f_ds = factor * exp2f(-Scaling<T>::kPShift);
 
     auto step = [&](int n, int run, auto masked) {
@@ -469,37 +498,67 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       else
         step(n, at.run, std::false_type{});
     }
-    mbar_wait(&sm.done, 0, 423);
+    if (n_all > 0) mbar_wait(&sm.done, 0, 423);
     tc_fence_after();
     // dV and dK: by a warpgroup each, or one after the other
     const int i = row_index(it, kt, r);
+    const int64_t row = static_cast<int64_t>(it.start) + i;
 #pragma unroll
     for (int w = 0; w < 2 / C::kWG; ++w) {
       const int which = C::kWG == 2 ? half : w;
       const uint32_t g_at = lane_base + (which == 0 ? kColDV : kColDK);
       const float scale = which == 0 ? exp2f(-Scaling<T>::kPShift) : a.tau / factor;
       const Out& out = a.out[which];
-      T* dst = reinterpret_cast<T*>(out.ptr) + (static_cast<int64_t>(it.start) + i) * out.ts +
-               kv_head * out.hs;
+      T* dst = reinterpret_cast<T*>(out.ptr) + row * out.ts + kv_head * out.hs;
+      float* part = a.splits > 1
+                        ? a.part + (((split * 2 + which) * a.tokens + row) * a.kv_heads + kv_head) * D
+                        : nullptr;
 #pragma unroll
       for (int cc = 0; cc < D; cc += 32) {
         uint32_t y[32];
         tmem_ld32(g_at + cc, y);
         tmem_ld_wait_regs32(y);
-        if (i >= 0) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * scale;
-            *reinterpret_cast<uint4*>(dst + cc + e) = pack8<T>(f);
-          }
-        }
+        if (i >= 0) store32<T>(y, n_all > 0, scale, dst + cc, part == nullptr ? nullptr : part + cc);
       }
     }
     tc_fence_before();
     named_barrier_sync(15, C::kThreads);
   }
+}
+
+// Outputs from the parts, added in their order: 8 channels per thread.
+struct JoinArgs {
+  const float* part;  // [splits][count][tokens][heads][D]
+  Out out[2];
+  int64_t tokens;
+  int heads, splits, count;
+};
+template <typename T, int D>
+__global__ void __launch_bounds__(256) join_kernel(const JoinArgs a) {
+  const int64_t n = a.tokens * a.heads * (D / 8);
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= a.count * n) return;
+  const int which = at >= n ? 1 : 0;
+  const int64_t v = at - which * n;  // vector of 8 channels
+  float f[8] = {};
+  for (int s = 0; s < a.splits; ++s) {
+    const float4* p =
+        reinterpret_cast<const float4*>(a.part + ((s * a.count + which) * n + v) * 8);
+    const float4 x = __ldcs(p), y = __ldcs(p + 1);
+    f[0] += x.x;
+    f[1] += x.y;
+    f[2] += x.z;
+    f[3] += x.w;
+    f[4] += y.x;
+    f[5] += y.y;
+    f[6] += y.z;
+    f[7] += y.w;
+  }
+  const int64_t vec = v / (D / 8), row = vec / a.heads;
+  const int head = static_cast<int>(vec - row * a.heads);
+  const Out& out = a.out[which];
+  *reinterpret_cast<uint4*>(reinterpret_cast<T*>(out.ptr) + row * out.ts + head * out.hs +
+                            8 * (v - vec * (D / 8))) = pack8<T>(f);
 }
 
 // ---- dQ -------------------------------------------------------------------------------------
@@ -535,17 +594,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   // TMEM columns: two S blocks (dS overwrites the one it came from), dP, dQ
   constexpr uint32_t kColDP = 2 * BN, kColDQ = 3 * BN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int head;
-  const Item it = grid_at(a.grid, head);
+  int grid_head;
+  const Item it = grid_at(a.grid, grid_head);
+  const int head = grid_head / a.splits, split = grid_head - head * a.splits;
   const int kv_head = head / a.group;
   const int tiles = tiles_of(it), pad = tiles * BT - it.len;
   // the steps' runs of keys: first .. first + runs - 1, in a sequence's first tile (or only one)
   // twice, the first `pre` steps for D
   const int first = pad / BN;
   const int runs = (a.causal ? it.tile + 1 : tiles) * (BT / BN) - first;
-  const int pre = runs * BN <= BT ? runs : 0;
-  const int n_all = pre + runs;
-  auto run_of = [&](int n) { return first + (n < pre ? n : n - pre); };
+  const bool twice = runs * BN <= BT;
+  // this part's: the walks that are made twice are short and stay whole, in part 0
+  const int from = twice ? 0 : static_cast<int>(static_cast<int64_t>(runs) * split / a.splits);
+  const int to = twice ? (split == 0 ? runs : 0)
+                       : static_cast<int>(static_cast<int64_t>(runs) * (split + 1) / a.splits);
+  const int pre = twice ? to : 0;
+  const int n_all = pre + to - from;
+  auto run_of = [&](int n) { return first + from + (n < pre ? n : n - pre); };
 
   if (threadIdx.x == 0) {
     sm.abort = device_aborted() ? 1 : 0;
@@ -578,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   if (warp >= C::kProducerWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
     if (warp == C::kProducerWarp) {
-      if (lane == 0) {
+      if (lane == 0 && n_all > 0) {
         mbar_arrive_expect_tx(&sm.q_full, 2 * BT * D * 2);
         load_tile<T, D, BN, BT>(sm.q, &tm_q, it, it.tile, head, &sm.q_full);
         load_tile<T, D, BN, BT>(sm.dout, &tm_do, it, it.tile, head, &sm.q_full);
@@ -596,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
-      {
+      if (n_all > 0) {
         const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
@@ -664,12 +729,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     // padding rows: P = exp2(-inf) = 0
     const float neg_shift =
         i >= 0 ? fmaf(a.lse[head * a.T + row], -kLog2e, Scaling<T>::kPShift) : -INFINITY;
-    float dvec = i >= 0 && pre == 0 ? a.dvec[head * a.T + row] : 0.0f;
+    float dvec = i >= 0 && !twice ? a.dvec[head * a.T + row] : 0.0f;
     const float c = a.scale_log2;
     float factor = 1.0f;
     if (Scaling<T>::kOn)
       factor = ds_factor(
-          a.norms + (static_cast<int64_t>(it.seq) * (a.grid.heads / a.group) + kv_head) * 2);
+          a.norms + (static_cast<int64_t>(it.seq) * a.kv_heads + kv_head) * 2);
     const float f_ds = factor * exp2f(-Scaling<T>::kPShift);
 
     auto step = [&](int n, auto masked) {
@@ -750,26 +815,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       else
         step(n, std::false_type{});
     }
-    mbar_wait(&sm.done, 0, 522);
+    if (n_all > 0) mbar_wait(&sm.done, 0, 522);
     tc_fence_after();
     // a warpgroup stores its part of the channels
     const float scale = a.tau / factor;
     T* dst = reinterpret_cast<T*>(a.out[0].ptr) + row * a.out[0].ts + head * a.out[0].hs;
+    float* part = a.splits > 1
+                      ? a.part + ((split * a.tokens + row) * (a.grid.heads / a.splits) + head) * D
+                      : nullptr;
 #pragma unroll
     for (int k0 = 0; k0 < D / C::kWG; k0 += 32) {
       const int cc = half * (D / C::kWG) + k0;
       uint32_t y[32];
       tmem_ld32(lane_base + kColDQ + cc, y);
       tmem_ld_wait_regs32(y);
-      if (i >= 0) {
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          float f[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * scale;
-          *reinterpret_cast<uint4*>(dst + cc + e) = pack8<T>(f);
-        }
-      }
+      if (i >= 0) store32<T>(y, n_all > 0, scale, dst + cc, part == nullptr ? nullptr : part + cc);
     }
     tc_fence_before();
     named_barrier_sync(15, C::kThreads);

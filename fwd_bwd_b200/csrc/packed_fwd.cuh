@@ -236,7 +236,92 @@ struct Args {
   int group;        // query heads per key head
   int causal;
   float scale_log2;  // softmax_scale log2(e)
+  // The walk over a tile's keys may be cut into `splits` parts: the grid then has splits x heads, and
+  // a part's unnormalized O goes to part [splits][tokens][Hq][D], its row maxima (log2 units) and
+  // sums to stats [splits][tokens][Hq][2].
+  int splits, heads;
+  float* part;
+  float2* stats;
+  int64_t tokens;
 };
+
+// A row's results: the output and LSE, or this part's share of them.  y: 32 channels from cc on of
+// the accumulated O.
+template <typename T>
+struct RowOut {
+  T* out;
+  float* part;
+  float inv_l;
+  __device__ __forceinline__ void store32(const uint32_t (&y)[32], int cc) const {
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * inv_l;
+      if (part == nullptr) {
+        *reinterpret_cast<uint4*>(out + cc + e) = pack8<T>(f);
+      } else {
+        *reinterpret_cast<float4*>(part + cc + e) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(part + cc + e + 4) = make_float4(f[4], f[5], f[6], f[7]);
+      }
+    }
+  }
+};
+template <typename T, int D>
+__device__ __forceinline__ RowOut<T> row_out(const Args& a, int64_t row, int head, int split,
+                                             float m, float l) {
+  RowOut<T> r;
+  r.out = reinterpret_cast<T*>(a.o.ptr) + row * a.o.ts + head * a.o.hs;
+  if (a.splits == 1) {
+    r.part = nullptr;
+    r.inv_l = 1.0f / l;
+    a.lse[head * a.T + row] = (m + log2f(l)) * 0.69314718055994531f;
+  } else {
+    const int64_t at = (split * a.tokens + row) * a.heads + head;
+    r.part = a.part + at * D;
+    r.inv_l = 1.0f;
+    a.stats[at] = make_float2(m, l);
+  }
+  return r;
+}
+
+// Output and LSE from the parts, in their order: 8 channels of a row per thread.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) merge_kernel(const Args a) {
+  const int64_t n = a.tokens * a.heads * (D / 8);
+  const int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (v >= n) return;
+  const int64_t vec = v / (D / 8), row = vec / a.heads;
+  const int head = static_cast<int>(vec - row * a.heads);
+  const int c0 = 8 * static_cast<int>(v - vec * (D / 8));
+  float m = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.stats[s * a.tokens * a.heads + vec].x);
+  const float shift = m == -INFINITY ? 0.0f : m;
+  float f[8] = {}, l = 0.0f;
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 t = a.stats[s * a.tokens * a.heads + vec];
+    if (t.y == 0.0f) continue;  // a part without keys has written no O
+    const float w = exp2f(t.x - shift);
+    l = fmaf(t.y, w, l);
+    const float4* p =
+        reinterpret_cast<const float4*>(a.part + (s * a.tokens * a.heads + vec) * D + c0);
+    const float4 x = __ldcs(p), y = __ldcs(p + 1);
+    f[0] = fmaf(x.x, w, f[0]);
+    f[1] = fmaf(x.y, w, f[1]);
+    f[2] = fmaf(x.z, w, f[2]);
+    f[3] = fmaf(x.w, w, f[3]);
+    f[4] = fmaf(y.x, w, f[4]);
+    f[5] = fmaf(y.y, w, f[5]);
+    f[6] = fmaf(y.z, w, f[6]);
+    f[7] = fmaf(y.w, w, f[7]);
+  }
+  const float inv_l = 1.0f / l;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] *= inv_l;
+  *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.o.ptr) + row * a.o.ts + head * a.o.hs + c0) =
+      pack8<T>(f);
+  if (c0 == 0) a.lse[head * a.T + row] = (m + log2f(l)) * 0.69314718055994531f;
+}
 
 // HEADS: the CTA's tiles are two heads of one group; otherwise tiles `tile` and `tile - 1` of one
 // head (the second absent when tile = 0).
@@ -250,15 +335,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   constexpr int NST = SM::NST;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int hg;
-  const Item it = grid_at(a.grid, hg);
+  int grid_head;
+  const Item it = grid_at(a.grid, grid_head);
+  const int hg = grid_head / a.splits, split = grid_head - hg * a.splits;
   const int head0 = HEADS ? 2 * hg : hg;
   const int kv_head = head0 / a.group;
   const bool two = HEADS || it.tile > 0;
   auto tile_of = [&](int g) { return HEADS ? it.tile : it.tile - g; };
   auto keys_of = [&](int g) { return a.causal ? tile_of(g) + 1 : tiles_of(it); };
-  const int n0 = keys_of(0);  // the most key tiles of the two
-  const int n1 = two ? keys_of(1) : 0;
+  // key tiles of this part, for tile 0 (the most) and tile 1: from .. from + n - 1
+  const int all = keys_of(0);
+  const int from = static_cast<int>(static_cast<int64_t>(all) * split / a.splits);
+  const int to = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / a.splits);
+  const int n0 = to - from;
+  const int n1 = two ? max(0, min(keys_of(1), to) - from) : 0;
 
   if (threadIdx.x == 0) {
     sm.abort = device_aborted() ? 1 : 0;
@@ -289,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     if (warp == kProducerWarp) {
-      if (lane == 0) {
+      if (lane == 0 && n0 > 0) {
         mbar_arrive_expect_tx(&sm.q_full, (two ? 2 : 1) * BT * D * 2);
         load_tile<T, D, D, BT>(sm.q[0], &tm_q, it, tile_of(0), head0, &sm.q_full);
         if (two)
@@ -302,12 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int j = v ? (i == 2 * n0 - 1 ? n0 - 1 : i / 2 - 1) : (i + 1) / 2;
           if (i >= NST) mbar_wait(&sm.empty[st], ring.parity ^ 1, 301);
           mbar_arrive_expect_tx(&sm.full[st], BT * D * 2);
-          load_tile<T, D, D, BT>(sm.kv[st], v ? &tm_v : &tm_k, it, j, kv_head, &sm.full[st]);
+          load_tile<T, D, D, BT>(sm.kv[st], v ? &tm_v : &tm_k, it, from + j, kv_head,
+                                 &sm.full[st]);
         }
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
-      {
+      if (n0 > 0) {
         const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
@@ -391,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (MASK) {
         // key index within the sequence must be >= 0 (the ragged first tile) and, when causal,
         // not above the row's
-        const int lo = -row_index(it, j, 0);
-        const int hi = a.causal ? i - row_index(it, j, 0) : BT - 1;
+        const int lo = -row_index(it, from + j, 0);
+        const int hi = a.causal ? i - row_index(it, from + j, 0) : BT - 1;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -462,34 +553,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const bool ragged = tiles_of(it) * BT != it.len;
     for (int j = 0; j < n; ++j) {
-      if ((j == 0 && ragged) || (a.causal && j == tile))
+      if ((from + j == 0 && ragged) || (a.causal && from + j == tile))
         block(j, std::true_type{});
       else
         block(j, std::false_type{});
     }
-    mbar_wait(&sm.o_full, 0, 321);
+    RowOut<T> res = {};
+    if (n0 > 0) mbar_wait(&sm.o_full, 0, 321);
     tc_fence_after();
-    if (n > 0) {
-      const int head = HEADS ? head0 + g : head0;
-      const float inv_l = 1.0f / l;
+    if (i >= 0 && (g == 0 || two)) {
       const int64_t row = static_cast<int64_t>(it.start) + i;
-      T* out = reinterpret_cast<T*>(a.o.ptr) + row * a.o.ts + head * a.o.hs;
+      res = row_out<T, D>(a, row, HEADS ? head0 + g : head0, split, m, l);
+    }
+    if (n > 0) {
 #pragma unroll
       for (int cc = 0; cc < D; cc += 32) {
         uint32_t y[32];
         tmem_ld32(o_at + cc, y);
         tmem_ld_wait_regs32(y);
-        if (i >= 0) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * inv_l;
-            *reinterpret_cast<uint4*>(out + cc + e) = pack8<T>(f);
-          }
-        }
+        if (i >= 0) res.store32(y, cc);
       }
-      if (i >= 0) a.lse[head * a.T + row] = (m + log2f(l)) * 0.69314718055994531f;
     }
     tc_fence_before();
     named_barrier_sync(15, kThreads);
@@ -526,12 +609,17 @@ __global__ void __launch_bounds__(kThreads64, 4)
   SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   constexpr uint32_t kColO64 = 64;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int head;
-  const Item it = grid_at(a.grid, head);
+  int grid_head;
+  const Item it = grid_at(a.grid, grid_head);
+  const int head = grid_head / a.splits, split = grid_head - head * a.splits;
   const int kv_head = head / a.group;
   const int tiles = tiles_of(it), pad = tiles * BT - it.len;
-  const int first = pad / BN;  // a run that is all padding is left out
-  const int n = (a.causal ? it.tile + 1 : tiles) * (BT / BN) - first;
+  const int ragged = pad / BN;  // first run of keys: one that is all padding is left out
+  const int runs = (a.causal ? it.tile + 1 : tiles) * (BT / BN) - ragged;
+  // this part's runs
+  const int from = static_cast<int>(static_cast<int64_t>(runs) * split / a.splits);
+  const int n = static_cast<int>(static_cast<int64_t>(runs) * (split + 1) / a.splits) - from;
+  const int first = ragged + from;
 
   if (threadIdx.x == 0) {
     sm.abort = device_aborted() ? 1 : 0;
@@ -557,7 +645,7 @@ __global__ void __launch_bounds__(kThreads64, 4)
   const uint32_t tmem = sm.tmem_base;
 
   if (warp == kIssueWarp64) {
-    {
+    if (n > 0) {
       const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
       constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
@@ -689,32 +777,24 @@ __global__ void __launch_bounds__(kThreads64, 4)
       l += (sum.x + sum.y) + (sum2.x + sum2.y);
     };
     for (int j = 0; j < n; ++j) {
-      if ((j == 0 && pad > 0) || (a.causal && first + j >= it.tile * (BT / BN)))
+      if ((first + j == ragged && pad > 0) || (a.causal && first + j >= it.tile * (BT / BN)))
         block(j, std::true_type{});
       else
         block(j, std::false_type{});
     }
-    mbar_wait(&sm.o_full, 0, 352);
+    if (n > 0) mbar_wait(&sm.o_full, 0, 352);
     tc_fence_after();
-    const float inv_l = 1.0f / l;
-    const int64_t row = static_cast<int64_t>(it.start) + i;
-    T* out = reinterpret_cast<T*>(a.o.ptr) + row * a.o.ts + head * a.o.hs;
+    RowOut<T> res = {};
+    if (i >= 0) res = row_out<T, D>(a, static_cast<int64_t>(it.start) + i, head, split, m, l);
+    if (n > 0) {
 #pragma unroll
-    for (int cc = 0; cc < D; cc += 32) {
-      uint32_t y[32];
-      tmem_ld32(o_at + cc, y);
-      tmem_ld_wait_regs32(y);
-      if (i >= 0) {
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          float f[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * inv_l;
-          *reinterpret_cast<uint4*>(out + cc + e) = pack8<T>(f);
-        }
+      for (int cc = 0; cc < D; cc += 32) {
+        uint32_t y[32];
+        tmem_ld32(o_at + cc, y);
+        tmem_ld_wait_regs32(y);
+        if (i >= 0) res.store32(y, cc);
       }
     }
-    if (i >= 0) a.lse[head * a.T + row] = (m + log2f(l)) * 0.69314718055994531f;
     tc_fence_before();
     named_barrier_sync(15, kThreads64);
   }

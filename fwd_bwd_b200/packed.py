@@ -105,13 +105,16 @@ def _check_batch(q: torch.Tensor, batch: Batch) -> None:
 
 
 def attn_fwd(q, k, v, batch: Batch, causal: bool = True, softmax_scale: float = 0.0, o=None,
-             lse=None) -> Tuple[torch.Tensor, torch.Tensor]:
+             lse=None, workspace: Optional[torch.Tensor] = None
+             ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention within each sequence (sage_packed_attn_fwd): (o [T, Hq, d], lse [Hq, T]).
 
     q: [T, Hq, d], k and v: [T, Hkv, d], CUDA fp16/bf16, any strides the kernels can read (slices
     of one projection); query head h reads key head h // (Hq / Hkv).  ``softmax_scale <= 0``
     selects 1/sqrt(d).  Rows behind the last sequence of ``o`` and ``lse`` are left as they are
     when the caller gives them, zero otherwise.  Given outputs must not overlap the inputs.
+    ``workspace``: a uint8 tensor of at least ``fwd_workspace_bytes`` elements (often none); calls
+    that share one must be ordered.
     """
     prm = _params(q, k, v, batch, causal, softmax_scale)
     _check_batch(q, batch)
@@ -124,8 +127,14 @@ def attn_fwd(q, k, v, batch: Batch, causal: bool = True, softmax_scale: float = 
         _check_lse(lse, q)
     rows_o = _like("o", o, q)
     if batch.tokens:
-        _call("sage_packed_attn_fwd", q.get_device(), batch._used_on, prm, batch.info, batch.plan_ptr, _rows(q),
-              _rows(k), _rows(v), rows_o, lse.data_ptr())
+        if workspace is None:
+            n = int(lib().sage_packed_attn_fwd_workspace_bytes(prm, batch.info))
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        else:
+            _check_workspace(workspace, q)
+        _call("sage_packed_attn_fwd", q.get_device(), batch._used_on, prm, batch.info,
+              batch.plan_ptr, _rows(q), _rows(k), _rows(v), rows_o, lse.data_ptr(),
+              *_workspace_args(workspace))
     return o, lse
 
 
@@ -149,21 +158,37 @@ def attn_bwd(q, k, v, o, lse, dout, batch: Batch, causal: bool = True, softmax_s
         return dq, dk, dv
     if workspace is None:
         workspace = torch.empty(_workspace_bytes(prm, batch), dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != q.get_device() or not workspace.is_contiguous():
-        raise ValueError("the workspace must be a contiguous tensor on q's device")
-    _call("sage_packed_attn_bwd", q.get_device(), batch._used_on, prm, batch.info, batch.plan_ptr, *rows,
-          lse.data_ptr(), rows_do, *grads, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+    else:
+        _check_workspace(workspace, q)
+    _call("sage_packed_attn_bwd", q.get_device(), batch._used_on, prm, batch.info, batch.plan_ptr,
+          *rows, lse.data_ptr(), rows_do, *grads, *_workspace_args(workspace))
     return dq, dk, dv
+
+
+def _check_workspace(workspace: torch.Tensor, q: torch.Tensor) -> None:
+    if workspace.get_device() != q.get_device() or not workspace.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on q's device")
+
+
+def _workspace_args(workspace: Optional[torch.Tensor]) -> Tuple[Optional[int], int]:
+    if workspace is None:
+        return None, 0
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _workspace_bytes(prm: SagePackedParams, batch: Batch) -> int:
     return int(lib().sage_packed_attn_bwd_workspace_bytes(prm, batch.info))
 
 
-def workspace_bytes(q, k, v, batch: Batch) -> int:
+def workspace_bytes(q, k, v, batch: Batch, causal: bool = True) -> int:
     """Bytes of scratch ``attn_bwd`` needs on these tensors."""
-    return _workspace_bytes(_params(q, k, v, batch, True, 0.0), batch)
+    return _workspace_bytes(_params(q, k, v, batch, causal, 0.0), batch)
+
+
+def fwd_workspace_bytes(q, k, v, batch: Batch, causal: bool = True) -> int:
+    """Bytes of scratch ``attn_fwd`` needs on these tensors (0 for most)."""
+    prm = _params(q, k, v, batch, causal, 0.0)
+    return int(lib().sage_packed_attn_fwd_workspace_bytes(prm, batch.info))
 
 
 class _PackedAttention(torch.autograd.Function):
@@ -189,4 +214,5 @@ def packed_attention(q, k, v, batch: Batch, causal: bool = True, softmax_scale: 
     return _PackedAttention.apply(q, k, v, batch, causal, softmax_scale)
 
 
-__all__ = ["Batch", "attn_bwd", "attn_fwd", "packed_attention", "workspace_bytes"]
+__all__ = ["Batch", "attn_bwd", "attn_fwd", "fwd_workspace_bytes", "packed_attention",
+           "workspace_bytes"]

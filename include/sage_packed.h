@@ -94,7 +94,7 @@ int sage_qk_norm_rope_bwd(const sage_rope_params* p, const sage_rows* q, const s
  * device (16-byte aligned) and gives that copy's address, with what fill returned in `info`, to
  * every call on batches of these lengths.  The plan is read-only. */
 typedef struct {
-  int sequences, tiles, pairs, longest; /* longest: tokens of the longest sequence */
+  int sequences, tiles, pairs, longest; /* longest: tokens of the longest sequence  */
   int64_t tokens;                       /* sum of the lengths */
   int64_t causal_steps, full_steps;     /* (query tile, key tile) pairs of one head */
 } sage_packed_info;
@@ -113,12 +113,18 @@ typedef struct {
 /* Forward: o = softmax(softmax_scale q k^T) v within each sequence; lse [Hq][T] float32, the
  * natural log-sum-exp of the scaled scores.  Products of 16-bit values summed in float32; P is
  * rounded to dtype for the product with v.  Rows behind the last sequence are neither read
- * nor written.  Sequences never affect each other, whatever their values. */
+ * nor written.  Sequences never affect each other, whatever their values (a non-finite value may
+ * reach any row of its own sequence).  The workspace (16-byte aligned) is needed where
+ * sage_packed_attn_fwd_workspace_bytes is not 0: few heads and long sequences, whose walks over
+ * the keys are cut into parts and joined. */
+size_t sage_packed_attn_fwd_workspace_bytes(const sage_packed_params* p,
+                                            const sage_packed_info* info);
 int sage_packed_attn_fwd(const sage_packed_params* p, const sage_packed_info* info,
                          const void* plan, const sage_rows* q, const sage_rows* k,
-                         const sage_rows* v, const sage_rows* o, float* lse, void* stream);
+                         const sage_rows* v, const sage_rows* o, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
-/* Backward from the forward's o and lse: dq, dk, dv.  A query head's score gradient is
+/* Backward from the forward's o and lse: dq, dk, dv (workspace 16-byte aligned).  A query head's score gradient is
  * rounded to dtype for its products; each key head's gradients sum over its query heads in
  * float32, in a fixed order: results are the same from call to call. */
 size_t sage_packed_attn_bwd_workspace_bytes(const sage_packed_params* p,

@@ -454,3 +454,52 @@ def test_batch_freed_while_another_stream_reads_it():
         assert ops.device_status() == 0 and junk
         for n, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
             assert torch.equal(x, want[n]), n
+
+
+@pytest.mark.parametrize("heads,lengths", [((8, 1), [1500, 40]), ((16, 2), [3000]), ((6, 1), [257, 0, 1024]),
+                                           ((1, 1), [4100])], ids=str)
+@pytest.mark.parametrize("d,dt", [(64, HF), (128, BF)])
+def test_few_key_heads(heads, lengths, d, dt):
+    """Few key tiles with long walks: dK and dV are made in parts and joined."""
+    q, k, v, do = _inputs(sum(lengths) + 3, *heads, d, dt, "fused", seed=70)
+    for causal in (True, False):
+        got = _run(q, k, v, do, lengths, causal)
+        _check(got, q, k, v, do, lengths, causal)
+        again = _run(q, k, v, do, lengths, causal)
+        for n in ("dk", "dv"):
+            assert torch.equal(got[n], again[n])
+            assert not got[n][sum(lengths):].any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_parts_keep_sequences_apart_and_nan_within(d):
+    """Walks cut into parts: another sequence's NaN stays there, its own reaches the rows that see
+    it (whole parts of NaN scores too), and rows of earlier tiles stay finite."""
+    lengths = [300, 4096]
+    q, k, v, do = _inputs(sum(lengths), 1, 1, d, BF, "plain", seed=71)
+    b = packed.Batch(lengths)
+    assert packed.fwd_workspace_bytes(q, k, v, b) > 0
+    clean = _run(q, k, v, do, lengths)
+    bad = k.clone()
+    bad[:300] = math.nan
+    got = _run(q, bad, v, do, lengths)
+    for n, x in got.items():
+        rows = (slice(None), slice(300, None)) if n == "lse" else slice(300, None)
+        assert torch.equal(x[rows], clean[n][rows]), n
+    bad = k.clone()
+    bad[300 + 1024:300 + 2304] = math.nan
+    o, lse = packed.attn_fwd(q, bad, v, b)
+    assert torch.isnan(o[300 + 1024:]).all() and torch.isnan(lse[:, 300 + 1024:]).all()
+    assert torch.equal(o[:300 + 1024], clean["o"][:300 + 1024])
+
+
+def test_workspace_refusals_of_the_forward():
+    q, k, v, _ = _inputs(4096, 1, 1, 64, BF, "plain")
+    b = packed.Batch([4096])
+    n = packed.fwd_workspace_bytes(q, k, v, b)
+    with pytest.raises(RuntimeError, match="WORKSPACE"):
+        packed.attn_fwd(q, k, v, b, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        packed.attn_fwd(q, k, v, b, workspace=torch.empty(n, dtype=torch.uint8))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert torch.equal(packed.attn_fwd(q, k, v, b, workspace=ws)[0], packed.attn_fwd(q, k, v, b)[0])

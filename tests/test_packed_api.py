@@ -30,7 +30,8 @@ def test_exports(L):
     src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
     names = sorted(set(re.findall(r"\b(sage_[a-z0-9_]+)\s*\(", src)))
     assert names == ["sage_packed_attn_bwd", "sage_packed_attn_bwd_workspace_bytes",
-                     "sage_packed_attn_fwd", "sage_packed_plan_bytes", "sage_packed_plan_fill",
+                     "sage_packed_attn_fwd", "sage_packed_attn_fwd_workspace_bytes",
+                     "sage_packed_plan_bytes", "sage_packed_plan_fill",
                      "sage_qk_norm_rope_bwd", "sage_qk_norm_rope_fwd",
                      "sage_qk_norm_rope_workspace_bytes"]
     for n in names:
@@ -106,7 +107,7 @@ def test_attention_refusals(L):
         p = SagePackedParams(*{**good, **(prm or {})}.values())
         r = {"q": _rows(4), "k": _rows(2), "v": _rows(2), "o": _rows(4), **rows}
         return L.sage_packed_attn_fwd(ctypes.byref(p), ctypes.byref(inf), plan, *r.values(), lse,
-                                      None)
+                                      None, 0, None)
 
     E = _lib
     for prm, code in ((dict(d=96), E.SAGE_ERR_UNSUPPORTED), (dict(d=256), E.SAGE_ERR_UNSUPPORTED),
@@ -133,7 +134,19 @@ def test_attention_refusals(L):
     empty = SagePackedInfo(2, 0, 0, 0, 0)
     assert fwd(inf=empty) == E.SAGE_OK
 
+    # few heads and a long sequence: parts, which need a workspace
     p = SagePackedParams(*good.values())
+    need = L.sage_packed_attn_fwd_workspace_bytes
+    assert need(ctypes.byref(p), ctypes.byref(info)) == 0
+    long = _info([128 * 100])
+    pl = SagePackedParams(*{**good, "T": 12800}.values())
+    n = need(ctypes.byref(pl), ctypes.byref(long))
+    assert n >= 2 * 12800 * 4 * (64 + 2) * 4
+    args = (ctypes.byref(pl), ctypes.byref(long), FAKE, _rows(4), _rows(2), _rows(2), _rows(4), FAKE)
+    assert L.sage_packed_attn_fwd(*args, None, 0, None) == E.SAGE_ERR_WORKSPACE
+    assert L.sage_packed_attn_fwd(*args, FAKE, n - 1, None) == E.SAGE_ERR_WORKSPACE
+    assert L.sage_packed_attn_fwd(*args, FAKE + 8, n, None) == E.SAGE_ERR_ALIGNMENT
+
     ws = L.sage_packed_attn_bwd_workspace_bytes(ctypes.byref(p), ctypes.byref(info))
     assert ws == 4 * 128 * 4
     half = SagePackedParams(*{**good, "dtype": 0}.values())
