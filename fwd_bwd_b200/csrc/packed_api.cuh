@@ -386,19 +386,28 @@ int run_packed_fwd(const sage_packed_params* p, const sage_packed_info* info, co
     const int ctas = p->Hq * w.splits;  // per item
     a.grid = {plan_list(plan, info, p->causal, false), info->tiles, ctas,
               grid_chunk(p, info, ctas, kv_bytes / a.group / w.splits)};
-    s = launch_packed<F::attn_fwd64_kernel<T>, 0>(static_cast<int64_t>(info->tiles) * ctas,
-                                                  F::kThreads64, F::smem64_bytes<T>(), st, tq, tk,
-                                                  tv, a);
+    const int64_t grid = static_cast<int64_t>(info->tiles) * ctas;
+    const size_t smem = F::smem64_bytes<T>();
+    s = w.splits > 1 ? launch_packed<F::attn_fwd64_kernel<T, true>, 0>(grid, F::kThreads64, smem, st,
+                                                                       tq, tk, tv, a)
+                     : launch_packed<F::attn_fwd64_kernel<T, false>, 0>(grid, F::kThreads64, smem,
+                                                                        st, tq, tk, tv, a);
   } else {
     const bool heads = a.group % 2 == 0;
     const int ctas = (heads ? p->Hq / 2 : p->Hq) * w.splits;  // per item
     a.grid = {plan_list(plan, info, p->causal, !heads), heads ? info->tiles : info->pairs, ctas,
               grid_chunk(p, info, ctas, kv_bytes / (heads ? a.group / 2 : a.group) / w.splits)};
     const int64_t grid = static_cast<int64_t>(a.grid.n_items) * ctas;
-    s = heads ? launch_packed<F::attn_fwd_kernel<T, D, true>, F::kLaunchRegs>(
-                    grid, F::kThreads, F::smem_bytes<T, D>(), st, tq, tk, tv, a)
-              : launch_packed<F::attn_fwd_kernel<T, D, false>, F::kLaunchRegs>(
-                    grid, F::kThreads, F::smem_bytes<T, D>(), st, tq, tk, tv, a);
+    const size_t smem = F::smem_bytes<T, D>();
+    auto launch = [&](auto by_heads, auto parts) {
+      return launch_packed<
+          F::attn_fwd_kernel<T, D, decltype(by_heads)::value, decltype(parts)::value>,
+          F::kLaunchRegs>(grid, F::kThreads, smem, st, tq, tk, tv, a);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    s = heads ? (w.splits > 1 ? launch(Yes{}, Yes{}) : launch(Yes{}, No{}))
+              : (w.splits > 1 ? launch(No{}, Yes{}) : launch(No{}, No{}));
   }
   if (s != SAGE_OK || w.splits == 1) return s;
   const int64_t vectors = info->tokens * p->Hq * (D / 8);
@@ -485,9 +494,13 @@ int run_packed_bwd(const sage_packed_params* p, const sage_packed_info* info, co
   a.grid = {r.items, info->tiles, heads,
             grid_chunk(p, info, heads, pair_bytes / r.group / a.splits)};
   a.out[0] = a.out[1] = packed_out(dq);
-  s = launch_packed<B::dq_kernel<T, D>, B::Cfg<D>::kLaunchRegs>(
-      static_cast<int64_t>(info->tiles) * heads, B::Cfg<D>::kThreads, B::dq_smem_bytes<T, D>(), st,
-      tq, tk, tv, tdo, a);
+  s = a.splits > 1
+          ? launch_packed<B::dq_kernel<T, D, true>, B::Cfg<D>::kLaunchRegs>(
+                static_cast<int64_t>(info->tiles) * heads, B::Cfg<D>::kThreads,
+                B::dq_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a)
+          : launch_packed<B::dq_kernel<T, D, false>, B::Cfg<D>::kLaunchRegs>(
+                static_cast<int64_t>(info->tiles) * heads, B::Cfg<D>::kThreads,
+                B::dq_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
   if (s == SAGE_OK && a.splits > 1) s = join(p->Hq, 1);
   if (s != SAGE_OK) return s;
   a.splits = w.dkv_splits;
@@ -496,9 +509,13 @@ int run_packed_bwd(const sage_packed_params* p, const sage_packed_info* info, co
             grid_chunk(p, info, heads, pair_bytes * r.group / a.splits)};
   a.out[0] = packed_out(dv);
   a.out[1] = packed_out(dk);
-  s = launch_packed<B::dkv_kernel<T, D>, B::Cfg<D>::kLaunchRegs>(
-      static_cast<int64_t>(info->tiles) * heads, B::Cfg<D>::kThreads, B::dkv_smem_bytes<T, D>(), st,
-      tq, tk, tv, tdo, a);
+  s = a.splits > 1
+          ? launch_packed<B::dkv_kernel<T, D, true>, B::Cfg<D>::kLaunchRegs>(
+                static_cast<int64_t>(info->tiles) * heads, B::Cfg<D>::kThreads,
+                B::dkv_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a)
+          : launch_packed<B::dkv_kernel<T, D, false>, B::Cfg<D>::kLaunchRegs>(
+                static_cast<int64_t>(info->tiles) * heads, B::Cfg<D>::kThreads,
+                B::dkv_smem_bytes<T, D>(), st, tq, tk, tv, tdo, a);
   if (s == SAGE_OK && a.splits > 1) s = join(p->Hkv, 2);
   return s;
 }

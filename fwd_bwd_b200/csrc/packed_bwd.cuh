@@ -218,7 +218,7 @@ __device__ __forceinline__ float2 pair_of(const float4& v, int e) {
 }
 
 // 32 sums of a row, scaled, to the output or, in float32, to a part (zeros for one without steps).
-template <typename T>
+template <typename T, bool PARTS>
 __device__ __forceinline__ void store32(const uint32_t (&y)[32], bool any, float scale, T* dst,
                                         float* part) {
 #pragma unroll
@@ -226,7 +226,7 @@ __device__ __forceinline__ void store32(const uint32_t (&y)[32], bool any, float
     float f[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = any ? __uint_as_float(y[e + k]) * scale : 0.0f;
-    if (part == nullptr) {
+    if (!PARTS) {
       *reinterpret_cast<uint4*>(dst + e) = pack8<T>(f);
     } else {
       *reinterpret_cast<float4*>(part + e) = make_float4(f[0], f[1], f[2], f[3]);
@@ -258,7 +258,9 @@ constexpr size_t dkv_smem_bytes() {
 static_assert(dkv_smem_bytes<__half, 128>() <= 232448 && dkv_smem_bytes<__half, 64>() <= 115712,
               "shared memory exceeds the limit");
 
-template <typename T, int D>
+// PARTS: the walks are cut into parts (Args::splits > 1); apart, because the others' code would
+// lose 4% to it.
+template <typename T, int D, bool PARTS>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -272,9 +274,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   // 64 h of their block, over columns that only the same warps have read.
   constexpr uint32_t kColDP = BN, kColDV = 2 * BN, kColDK = 2 * BN + D;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = PARTS ? a.splits : 1;
   int grid_head;
   const Item it = grid_at(a.grid, grid_head);
-  const int kv_head = grid_head / a.splits, split = grid_head - kv_head * a.splits;
+  const int kv_head = grid_head / splits, split = grid_head - kv_head * splits;
   const int tiles = tiles_of(it);
   // under a causal mask the list's order (most work first) is by query tile: mirrored for keys
   const int kt = a.causal ? tiles - 1 - it.tile : it.tile;
@@ -284,9 +287,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   const int first = max(a.causal ? diag : 0, pad / BN);
   // this part's steps of the walk over every head's runs
   const int walk = (runs - first) * a.group;
-  const int n_from = static_cast<int>(static_cast<int64_t>(walk) * split / a.splits);
+  const int n_from = static_cast<int>(static_cast<int64_t>(walk) * split / splits);
   const int n_all =
-      static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / a.splits) - n_from;
+      static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / splits) - n_from;
   // the steps' (query head, run of query rows), in order
   struct Walk {
     int head, run, first, runs;
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   if (warp >= C::kProducerWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
     if (warp == C::kProducerWarp) {
-      if (lane == 0 && n_all > 0) {
+      if (lane == 0 && (!PARTS || n_all > 0)) {
         mbar_arrive_expect_tx(&sm.kv_full, 2 * BT * D * 2);
         load_tile<T, D, BN, BT>(sm.k, &tm_k, it, kt, kv_head, &sm.kv_full);
         load_tile<T, D, BN, BT>(sm.v, &tm_v, it, kt, kv_head, &sm.kv_full);
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
-      if (n_all > 0) {
+      if ((!PARTS || n_all > 0)) {
         const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       else
         step(n, at.run, std::false_type{});
     }
-    if (n_all > 0) mbar_wait(&sm.done, 0, 423);
+    if ((!PARTS || n_all > 0)) mbar_wait(&sm.done, 0, 423);
     tc_fence_after();
     // dV and dK: by a warpgroup each, or one after the other
     const int i = row_index(it, kt, r);
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       const float scale = which == 0 ? exp2f(-Scaling<T>::kPShift) : a.tau / factor;
       const Out& out = a.out[which];
       T* dst = reinterpret_cast<T*>(out.ptr) + row * out.ts + kv_head * out.hs;
-      float* part = a.splits > 1
+      float* part = PARTS
                         ? a.part + (((split * 2 + which) * a.tokens + row) * a.kv_heads + kv_head) * D
                         : nullptr;
 #pragma unroll
@@ -518,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
         uint32_t y[32];
         tmem_ld32(g_at + cc, y);
         tmem_ld_wait_regs32(y);
-        if (i >= 0) store32<T>(y, n_all > 0, scale, dst + cc, part == nullptr ? nullptr : part + cc);
+        if (i >= 0) store32<T, PARTS>(y, (!PARTS || n_all > 0), scale, dst + cc, PARTS ? part + cc : nullptr);
       }
     }
     tc_fence_before();
@@ -581,7 +584,7 @@ constexpr size_t dq_smem_bytes() {
 static_assert(dq_smem_bytes<__half, 128>() <= 232448 && dq_smem_bytes<__half, 64>() <= 115712,
               "shared memory exceeds the limit");
 
-template <typename T, int D>
+template <typename T, int D, bool PARTS>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -594,9 +597,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   // TMEM columns: two S blocks (dS overwrites the one it came from), dP, dQ
   constexpr uint32_t kColDP = 2 * BN, kColDQ = 3 * BN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = PARTS ? a.splits : 1;
   int grid_head;
   const Item it = grid_at(a.grid, grid_head);
-  const int head = grid_head / a.splits, split = grid_head - head * a.splits;
+  const int head = grid_head / splits, split = grid_head - head * splits;
   const int kv_head = head / a.group;
   const int tiles = tiles_of(it), pad = tiles * BT - it.len;
   // the steps' runs of keys: first .. first + runs - 1, in a sequence's first tile (or only one)
@@ -605,9 +609,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   const int runs = (a.causal ? it.tile + 1 : tiles) * (BT / BN) - first;
   const bool twice = runs * BN <= BT;
   // this part's: the walks that are made twice are short and stay whole, in part 0
-  const int from = twice ? 0 : static_cast<int>(static_cast<int64_t>(runs) * split / a.splits);
+  const int from = twice ? 0 : static_cast<int>(static_cast<int64_t>(runs) * split / splits);
   const int to = twice ? (split == 0 ? runs : 0)
-                       : static_cast<int>(static_cast<int64_t>(runs) * (split + 1) / a.splits);
+                       : static_cast<int>(static_cast<int64_t>(runs) * (split + 1) / splits);
   const int pre = twice ? to : 0;
   const int n_all = pre + to - from;
   auto run_of = [&](int n) { return first + from + (n < pre ? n : n - pre); };
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   if (warp >= C::kProducerWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
     if (warp == C::kProducerWarp) {
-      if (lane == 0 && n_all > 0) {
+      if (lane == 0 && (!PARTS || n_all > 0)) {
         mbar_arrive_expect_tx(&sm.q_full, 2 * BT * D * 2);
         load_tile<T, D, BN, BT>(sm.q, &tm_q, it, it.tile, head, &sm.q_full);
         load_tile<T, D, BN, BT>(sm.dout, &tm_do, it, it.tile, head, &sm.q_full);
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
-      if (n_all > 0) {
+      if ((!PARTS || n_all > 0)) {
         const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
@@ -737,7 +741,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           a.norms + (static_cast<int64_t>(it.seq) * a.kv_heads + kv_head) * 2);
     const float f_ds = factor * exp2f(-Scaling<T>::kPShift);
 
-    auto step = [&](int n, auto masked) {
+    const int keys0 = row_index<BN>(it, first + from, 64 * half);
+    auto step = [&](int n, int key0, auto masked) {
       constexpr bool MASK = decltype(masked)::value;
       const uint32_t s_at = lane_base + BN * (n & 1) + 64 * half;
       const uint32_t dp_at = lane_base + kColDP + 64 * half;
@@ -748,7 +753,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       tmem_ld32(s_at + 32, x[1]);
       tmem_ld_wait_regs32(x[0]);
       tie32(x[1]);
-      const int key0 = row_index<BN>(it, run_of(n), 64 * half);
       const int last = a.causal ? i : 0x7fffffff;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -808,20 +812,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       tc_fence_before();
       mbar_arrive_warp(&sm.ds_ready[n & 1], lane);
     };
-    for (int n = 0; n < n_all; ++n) {
-      const int run = run_of(n);
-      if ((run == first && pad > 0) || (a.causal && run >= it.tile * (BT / BN)))
-        step(n, std::true_type{});
+    // runs that need a mask, from this part's first: the ragged first and the causal diagonal
+    const int ragged = from == 0 && pad > 0 ? 0 : -1;
+    const int diag = a.causal ? it.tile * (BT / BN) - first - from : 0x7fffffff;
+    for (int n = 0, run = 0; n < n_all; ++n) {
+      if (run == ragged || run >= diag)
+        step(n, keys0 + run * BN, std::true_type{});
       else
-        step(n, std::false_type{});
+        step(n, keys0 + run * BN, std::false_type{});
+      if (++run == to - from) run = 0;  // the second time
     }
-    if (n_all > 0) mbar_wait(&sm.done, 0, 522);
+    if ((!PARTS || n_all > 0)) mbar_wait(&sm.done, 0, 522);
     tc_fence_after();
     // a warpgroup stores its part of the channels
     const float scale = a.tau / factor;
     T* dst = reinterpret_cast<T*>(a.out[0].ptr) + row * a.out[0].ts + head * a.out[0].hs;
-    float* part = a.splits > 1
-                      ? a.part + ((split * a.tokens + row) * (a.grid.heads / a.splits) + head) * D
+    float* part = PARTS
+                      ? a.part + ((split * a.tokens + row) * (a.grid.heads / splits) + head) * D
                       : nullptr;
 #pragma unroll
     for (int k0 = 0; k0 < D / C::kWG; k0 += 32) {
@@ -829,7 +836,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       uint32_t y[32];
       tmem_ld32(lane_base + kColDQ + cc, y);
       tmem_ld_wait_regs32(y);
-      if (i >= 0) store32<T>(y, n_all > 0, scale, dst + cc, part == nullptr ? nullptr : part + cc);
+      if (i >= 0) store32<T, PARTS>(y, (!PARTS || n_all > 0), scale, dst + cc, PARTS ? part + cc : nullptr);
     }
     tc_fence_before();
     named_barrier_sync(15, C::kThreads);

@@ -247,7 +247,7 @@ struct Args {
 
 // A row's results: the output and LSE, or this part's share of them.  y: 32 channels from cc on of
 // the accumulated O.
-template <typename T>
+template <typename T, bool PARTS>
 struct RowOut {
   T* out;
   float* part;
@@ -258,7 +258,7 @@ struct RowOut {
       float f[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[e + k]) * inv_l;
-      if (part == nullptr) {
+      if (!PARTS) {
         *reinterpret_cast<uint4*>(out + cc + e) = pack8<T>(f);
       } else {
         *reinterpret_cast<float4*>(part + cc + e) = make_float4(f[0], f[1], f[2], f[3]);
@@ -267,12 +267,12 @@ struct RowOut {
     }
   }
 };
-template <typename T, int D>
-__device__ __forceinline__ RowOut<T> row_out(const Args& a, int64_t row, int head, int split,
+template <typename T, int D, bool PARTS>
+__device__ __forceinline__ RowOut<T, PARTS> row_out(const Args& a, int64_t row, int head, int split,
                                              float m, float l) {
-  RowOut<T> r;
+  RowOut<T, PARTS> r;
   r.out = reinterpret_cast<T*>(a.o.ptr) + row * a.o.ts + head * a.o.hs;
-  if (a.splits == 1) {
+  if (!PARTS) {
     r.part = nullptr;
     r.inv_l = 1.0f / l;
     a.lse[head * a.T + row] = (m + log2f(l)) * 0.69314718055994531f;
@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const Args a) {
 
 // HEADS: the CTA's tiles are two heads of one group; otherwise tiles `tile` and `tile - 1` of one
 // head (the second absent when tile = 0).
-template <typename T, int D, bool HEADS>
+// PARTS: the walks are cut into parts (Args::splits > 1).
+template <typename T, int D, bool HEADS, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k,
@@ -335,9 +336,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   constexpr int NST = SM::NST;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = PARTS ? a.splits : 1;
   int grid_head;
   const Item it = grid_at(a.grid, grid_head);
-  const int hg = grid_head / a.splits, split = grid_head - hg * a.splits;
+  const int hg = grid_head / splits, split = grid_head - hg * splits;
   const int head0 = HEADS ? 2 * hg : hg;
   const int kv_head = head0 / a.group;
   const bool two = HEADS || it.tile > 0;
@@ -345,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto keys_of = [&](int g) { return a.causal ? tile_of(g) + 1 : tiles_of(it); };
   // key tiles of this part, for tile 0 (the most) and tile 1: from .. from + n - 1
   const int all = keys_of(0);
-  const int from = static_cast<int>(static_cast<int64_t>(all) * split / a.splits);
-  const int to = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / a.splits);
+  const int from = static_cast<int>(static_cast<int64_t>(all) * split / splits);
+  const int to = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / splits);
   const int n0 = to - from;
   const int n1 = two ? max(0, min(keys_of(1), to) - from) : 0;
 
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     if (warp == kProducerWarp) {
-      if (lane == 0 && n0 > 0) {
+      if (lane == 0 && (!PARTS || n0 > 0)) {
         mbar_arrive_expect_tx(&sm.q_full, (two ? 2 : 1) * BT * D * 2);
         load_tile<T, D, D, BT>(sm.q[0], &tm_q, it, tile_of(0), head0, &sm.q_full);
         if (two)
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
-      if (n0 > 0) {
+      if (!PARTS || n0 > 0) {
         const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
         constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BT);
@@ -558,12 +560,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         block(j, std::false_type{});
     }
-    RowOut<T> res = {};
-    if (n0 > 0) mbar_wait(&sm.o_full, 0, 321);
+    RowOut<T, PARTS> res = {};
+    if (!PARTS || n0 > 0) mbar_wait(&sm.o_full, 0, 321);
     tc_fence_after();
     if (i >= 0 && (g == 0 || two)) {
       const int64_t row = static_cast<int64_t>(it.start) + i;
-      res = row_out<T, D>(a, row, HEADS ? head0 + g : head0, split, m, l);
+      res = row_out<T, D, PARTS>(a, row, HEADS ? head0 + g : head0, split, m, l);
     }
     if (n > 0) {
 #pragma unroll
@@ -598,7 +600,7 @@ constexpr size_t smem64_bytes() {
 static_assert(4 * (smem64_bytes<__half>() + 1024) <= 233472,
               "shared memory of four CTAs exceeds the limit");
 
-template <typename T>
+template <typename T, bool PARTS>
 __global__ void __launch_bounds__(kThreads64, 4)
     attn_fwd64_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -609,16 +611,17 @@ __global__ void __launch_bounds__(kThreads64, 4)
   SM& sm = *reinterpret_cast<SM*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   constexpr uint32_t kColO64 = 64;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = PARTS ? a.splits : 1;
   int grid_head;
   const Item it = grid_at(a.grid, grid_head);
-  const int head = grid_head / a.splits, split = grid_head - head * a.splits;
+  const int head = grid_head / splits, split = grid_head - head * splits;
   const int kv_head = head / a.group;
   const int tiles = tiles_of(it), pad = tiles * BT - it.len;
   const int ragged = pad / BN;  // first run of keys: one that is all padding is left out
   const int runs = (a.causal ? it.tile + 1 : tiles) * (BT / BN) - ragged;
   // this part's runs
-  const int from = static_cast<int>(static_cast<int64_t>(runs) * split / a.splits);
-  const int n = static_cast<int>(static_cast<int64_t>(runs) * (split + 1) / a.splits) - from;
+  const int from = static_cast<int>(static_cast<int64_t>(runs) * split / splits);
+  const int n = static_cast<int>(static_cast<int64_t>(runs) * (split + 1) / splits) - from;
   const int first = ragged + from;
 
   if (threadIdx.x == 0) {
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(kThreads64, 4)
   const uint32_t tmem = sm.tmem_base;
 
   if (warp == kIssueWarp64) {
-    if (n > 0) {
+    if (!PARTS || n > 0) {
       const uint32_t leader = elect_one(), tmem = uniform(sm.tmem_base);
       constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t id_s = instr_desc(1, kFmt, kFmt, false, false, BT, BN);
@@ -782,11 +785,11 @@ __global__ void __launch_bounds__(kThreads64, 4)
       else
         block(j, std::false_type{});
     }
-    if (n > 0) mbar_wait(&sm.o_full, 0, 352);
+    if (!PARTS || n > 0) mbar_wait(&sm.o_full, 0, 352);
     tc_fence_after();
-    RowOut<T> res = {};
-    if (i >= 0) res = row_out<T, D>(a, static_cast<int64_t>(it.start) + i, head, split, m, l);
-    if (n > 0) {
+    RowOut<T, PARTS> res = {};
+    if (i >= 0) res = row_out<T, D, PARTS>(a, static_cast<int64_t>(it.start) + i, head, split, m, l);
+    if (!PARTS || n > 0) {
 #pragma unroll
       for (int cc = 0; cc < D; cc += 32) {
         uint32_t y[32];
