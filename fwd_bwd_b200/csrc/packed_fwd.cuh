@@ -38,14 +38,15 @@
 // 222 us, 224 us with an eighth, 225 us with none; d = 64, images: 38 us against 39 us).
 //
 // Measured (B200, kernel time; causal, 2 products counted over the visible scores):
-//   d = 128, 16384 tokens, 32 / 8 heads, bf16                1643 us, 1338 TFLOP/s
-//   d = 128, 4 x 8192, 16 heads                               868 us, 1267 TFLOP/s
-//   d = 64, 8 x 2048, 16 heads                                112 us,  614 TFLOP/s
+//   d = 128, 16384 tokens, 32 / 8 heads, bf16                1627 us, 1352 TFLOP/s
+//   d = 128, 4 x 8192, 16 heads                               851 us, 1293 TFLOP/s
+//   d = 64, 8 x 2048, 16 heads                                111 us,  620 TFLOP/s
 // (cuBLAS bf16: 1614 TFLOP/s for a moment, 1368 under the power cap, which the first two reach
-// after some milliseconds: 1896 us in a loop.)  Bound: d = 128 by the chain S -> softmax -> P V of
-// two tiles that take turns (tensor pipe 56% active, special-function unit 56%); d = 64 by the
-// exponentials and the instructions around them (special-function unit 60%, tensor pipe 30%), with
-// a fixed 28 us for setting up and storing 2048 CTAs, partly hidden by the four to an SM.
+// after some milliseconds: 1871 us in a loop.)  Bound: d = 128 by the chain S -> softmax -> P V of
+// two tiles that take turns (tensor pipe 58% active, special-function unit 45%); d = 64 by the
+// exponentials and the instructions around them (issue 50%, special-function unit 49%, tensor
+// pipe 31%), with a fixed 28 us for setting up and storing 2048 CTAs, partly hidden by the four to
+// an SM.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -14,7 +14,7 @@
 // flight; each of its threads copies its own channels kAhead rows ahead into shared memory that
 // only it reads (no barrier: its own copy groups order it).
 //
-// Measured (B200): 262144 tokens, 20 heads of 128: forward 458 us (5.9 TB/s), backward 830 us (4.9
+// Measured (B200): 262144 tokens, 20 heads of 128: forward 459 us (5.8 TB/s), backward 836 us (4.8
 // TB/s, against 875 us with rows loaded to registers where they are used); 16384 tokens, 32 heads
 // of 64: 30 us and 46 us; a copy runs at 6.5 TB/s.  What keeps the backward from that is
 // instructions (180 per two rows of 128 channels, 61% of the issue slots, 16 warps to an SM).
