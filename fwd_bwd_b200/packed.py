@@ -22,7 +22,8 @@ class Batch:
 
     ``lengths``: a sequence of ints or a CPU integer tensor.  The plan (a list of the sequences'
     tiles, largest work first) is made on the host and copied to the device once; keep the
-    Batch for every layer and step on the same lengths.  Calls only read it.
+    Batch for every layer and step on the same lengths.  Calls only read it.  Make it outside of
+    graph captures (it waits for the copy) and keep it as long as a captured graph that uses it.
     """
 
     def __init__(self, lengths: Sequence[int], device="cuda"):

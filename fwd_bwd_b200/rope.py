@@ -175,8 +175,8 @@ def qk_norm_rope_fwd(q, k, positions, rope: Rope, gain_q=None, gain_k=None, q_ou
 
     q, k: CUDA fp16/bf16 [T, H, d] or [B, H, N, d], any strides the kernels can read (slices of
     one projection); positions: int32/int64 [N] or, with several axes, [axes, N] (for batched q
-    and k also [B, N] or [axes, B, N]); gains: float32 [d] or None for ones.  Outputs given by
-    the caller must not overlap the inputs.
+    and k also [B, N] or [axes, B, N]); gains: float32 [d], 16-byte aligned, or None for ones.
+    Outputs given by the caller must not overlap the inputs.
     """
     prm, pos = _params(q, k, positions, rope, (gain_q, gain_k))
     q_out = _new(q) if q_out is None else q_out
@@ -225,6 +225,7 @@ class _QkNormRope(torch.autograd.Function):
         q = q if _supported(q) else q.contiguous()
         k = k if _supported(k) else k.contiguous()
         gains = [None if g is None else g.detach().float().contiguous() for g in (gain_q, gain_k)]
+        gains = [g if g is None or g.data_ptr() % 16 == 0 else g.clone() for g in gains]
         ctx.save_for_backward(q, k, positions, *gains)
         ctx.rope = rope
         ctx.gain_dtypes = [None if g is None else g.dtype for g in (gain_q, gain_k)]

@@ -245,3 +245,24 @@ def test_no_tokens():
     assert y.shape == (0, 2, 64) and yk.shape == (0, 1, 64)
     *_, dgq, dgk = rope.qk_norm_rope_bwd(q, k, dy, dyk, pos, rp, *gains)
     assert not dgq.any() and not dgk.any()
+
+
+@pytest.mark.parametrize("d,hq,hkv,inter", [(64, 5, 3, False), (128, 6, 1, True)])
+def test_many_units_per_block(d, hq, hkv, inter):
+    """Every block walks many tiles of tokens, with odd numbers of heads."""
+    T = 30011
+    q, k, dy, dyk, gains = _case(T, hq, hkv, d, BF, 10)
+    pos = torch.randint(0, 1 << 17, (1, T), device="cuda", dtype=torch.int32)
+    _check(q, k, dy, dyk, gains, pos, rope.Rope(d, interleaved=inter))
+
+
+def test_gains_of_any_place_and_type_in_autograd():
+    q, k, dy, dyk, gains = _case(33, 2, 1, 64, BF, 11, "heads")
+    pos, rp = torch.arange(33, device="cuda"), rope.Rope(64)
+    store = torch.cat([torch.zeros(1, device="cuda"), *gains]).requires_grad_(True)
+    a, b = rope.qk_norm_rope(q, k, pos, rp, store[1:65], store[65:])  # not 16-byte aligned
+    (a.float() * dy.float()).sum().add((b.float() * dyk.float()).sum()).backward()
+    *_, dgq, dgk = rope.qk_norm_rope_bwd(q, k, dy, dyk, pos, rp, *gains)
+    assert torch.equal(store.grad[1:], torch.cat([dgq, dgk]))
+    with pytest.raises(RuntimeError, match="ALIGNMENT"):
+        rope.qk_norm_rope_fwd(q, k, pos, rp, store.detach()[1:65], gains[1])
