@@ -75,7 +75,8 @@ def _params(q, k, v, batch: Batch, causal: bool, softmax_scale: float) -> SagePa
     dtype, dev = _type_and_device(q)
     (T, Hq, d), (Tk, Hkv, dk) = q.shape, k.shape
     if k.shape != v.shape or Tk != T or dk != d:
-        raise ValueError("q, k and v must hold the same tokens and channels, k and v the same heads")
+        raise ValueError("q, k and v must hold the same tokens and channels, k and v the same "
+                         "heads")
     if (q.dtype != k.dtype or q.dtype != v.dtype or k.get_device() != dev
             or v.get_device() != dev):
         raise ValueError("q, k and v must have one type and device")
@@ -112,7 +113,10 @@ def attn_fwd(q, k, v, batch: Batch, causal: bool = True, softmax_scale: float = 
 
     q: [T, Hq, d], k and v: [T, Hkv, d], CUDA fp16/bf16, any strides the kernels can read (slices
     of one projection); query head h reads key head h // (Hq / Hkv).  ``softmax_scale <= 0``
-    selects 1/sqrt(d).  Rows behind the last sequence of ``o`` and ``lse`` are left as they are
+    selects 1/sqrt(d).  Sequences never touch each other, not even through NaN.  Within one, a
+    hidden key weighs exactly zero, so NaN or infinity in its v reaches the rows of its tile of 128
+    tokens (cut from the sequence's end) as 0 * inf; rows of earlier tiles do not see it.
+    Rows behind the last sequence of ``o`` and ``lse`` are left as they are
     when the caller gives them, zero otherwise.  Given outputs must not overlap the inputs.
     ``workspace``: a uint8 tensor of at least ``fwd_workspace_bytes`` elements (often none); calls
     that share one must be ordered.

@@ -503,3 +503,24 @@ def test_workspace_refusals_of_the_forward():
         packed.attn_fwd(q, k, v, b, workspace=torch.empty(n, dtype=torch.uint8))
     ws = torch.empty(n, dtype=torch.uint8, device="cuda")
     assert torch.equal(packed.attn_fwd(q, k, v, b, workspace=ws)[0], packed.attn_fwd(q, k, v, b)[0])
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (3, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_later_values_that_are_not_finite(d, Hq, Hkv):
+    """Of a hidden key: its k reaches no earlier row, its v none of the tiles before its own (tiles
+    of 128 from the sequence's end: 500 tokens start theirs at -12, 116, 244, 372)."""
+    q, k, v, _ = _inputs(500, Hq, Hkv, d, BF, "plain", seed=72)
+    b = packed.Batch([500])
+    o, lse = packed.attn_fwd(q, k, v, b)
+    for value in (math.nan, math.inf):
+        bad = k.clone()
+        bad[300] = value
+        o1, lse1 = packed.attn_fwd(q, bad, v, b)
+        assert torch.equal(o1[:300], o[:300]) and torch.equal(lse1[:, :300], lse[:, :300])
+        assert torch.isnan(o1[300:]).any(-1).any()
+        bad = v.clone()
+        bad[300] = value
+        o2, lse2 = packed.attn_fwd(q, k, bad, b)
+        assert torch.equal(o2[:244], o[:244]) and torch.equal(lse2, lse)
+        assert not torch.isfinite(o2[300:]).any()
