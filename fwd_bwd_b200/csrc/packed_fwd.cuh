@@ -182,13 +182,15 @@ struct Ring {
   }
 };
 
-// 2^z for a pair as in exp2_poly2, for z <= 127 of unmasked scores: below 2^-126 the result is
-// 2^-126 instead of zero.
+// 2^z for a pair as in exp2_poly2, for z <= 127 or NaN.  Below 2^-126 the exponent field runs out at
+// -127 and the result is off by up to 2^-127; -inf gives 2^-149, zero in 16 bits.  NaN passes the
+// clamp and the polynomial, and the exponent's addition makes it the largest float, infinity in 16
+// bits: with P that is not finite, neither are the sums it enters.
 __device__ __forceinline__ float2 exp2_fma2(float2 z) {
   constexpr float kC0 = 1.0000001192092896f, kC1 = 0.6931469440460205f,
                   kC2 = 0.24022120237350464f, kC3 = 0.05550713092088699f,
                   kC4 = 0.009675540961325169f, kC5 = 0.0013276472454890609f;
-  const float2 zc = make_float2(fmaxf(z.x, -126.0f), fmaxf(z.y, -126.0f));
+  const float2 zc = make_float2(fmax_nan(z.x, -127.0f), fmax_nan(z.y, -127.0f));
   const float2 t = __fadd2_rn(zc, make_float2(kMagic, kMagic));
   const float2 j = __fadd2_rn(t, make_float2(-kMagic, -kMagic));
   const float2 f = __ffma2_rn(j, make_float2(-1.0f, -1.0f), zc);
