@@ -33,6 +33,8 @@
 // Both: the running maximum that P is taken against is raised (and O rescaled in TMEM) only when
 // a row's maximum grows by more than 2^8: P then stays below 256, exact in the final division
 // by the row sum, and most key tiles leave O untouched.
+// A row that sees a score of NaN or +inf is NaN in O and LSE: the maximum keeps NaN, and the row's
+// exponentials, sum and rescaled O are NaN from that tile on.
 // Rounding: P to the tensors' type for P V (the sum l uses the unrounded P); O once at the end.
 // A quarter of the exponentials runs on the FMA pipe (32 heads of 128, prompts of 4099 to 8 tokens:
 // 222 us, 224 us with an eighth, 225 us with none; d = 64, images: 38 us against 39 us).
@@ -201,6 +203,12 @@ __device__ __forceinline__ float2 exp2_fma2(float2 z) {
   q = __ffma2_rn(q, f, make_float2(kC0, kC0));
   return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
                      __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// What the scores of a row are shifted by: -m; 0 while no key weighs anything (m = -inf), so that
+// -inf stays -inf; NaN for a maximum of +inf, whose row has no softmax.
+__device__ __forceinline__ float neg_max(float m) {
+  return m == -INFINITY ? 0.0f : fmaf(m, 0.0f, -m);
 }
 
 // Pairs whose exponentials run on the FMA pipe.
@@ -498,13 +506,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        mx[q] = fmaxf(__uint_as_float(x[q][0]), __uint_as_float(x[q][1]));
+        mx[q] = fmax_nan(__uint_as_float(x[q][0]), __uint_as_float(x[q][1]));
 #pragma unroll
         for (int e = 2; e < 32; e += 2)
-          mx[q] = fmax3(mx[q], __uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]));
+          mx[q] = fmax3_nan(mx[q], __uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1]));
       }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      const bool grow = top > m + 8.0f;  // always on the first tile with a visible key
+      const float top = fmax_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3]) * c;
+      // always on the first tile with a visible key, and from the first NaN on
+      const bool grow = !(top <= m + 8.0f);
       if (__any_sync(0xffffffffu, grow)) {
         const float mn = grow ? top : m;
         const float alpha = grow ? ex2_approx(m - mn) : 1.0f;
@@ -523,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const float neg = m == -INFINITY ? 0.0f : -m;
+      const float neg = neg_max(m);
       const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
       float2 sum = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -732,13 +741,14 @@ __global__ void __launch_bounds__(kThreads64, 4)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t* y = &x[q >> 1][16 * (q & 1)];
-        mx[q] = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+        mx[q] = fmax_nan(__uint_as_float(y[0]), __uint_as_float(y[1]));
 #pragma unroll
         for (int e = 2; e < 16; e += 2)
-          mx[q] = fmax3(mx[q], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+          mx[q] = fmax3_nan(mx[q], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
       }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      const bool grow = top > m + 8.0f;  // always on the first run with a visible key
+      const float top = fmax_nan(fmax3_nan(mx[0], mx[1], mx[2]), mx[3]) * c;
+      // always on the first run with a visible key, and from the first NaN on
+      const bool grow = !(top <= m + 8.0f);
       if (__any_sync(0xffffffffu, grow)) {
         const float mn = grow ? top : m;
         const float alpha = grow ? ex2_approx(m - mn) : 1.0f;
@@ -757,7 +767,7 @@ __global__ void __launch_bounds__(kThreads64, 4)
           }
         }
       }
-      const float neg = m == -INFINITY ? 0.0f : -m;
+      const float neg = neg_max(m);
       const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
       float2 sum = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll

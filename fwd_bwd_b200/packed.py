@@ -113,7 +113,8 @@ def attn_fwd(q, k, v, batch: Batch, causal: bool = True, softmax_scale: float = 
 
     q: [T, Hq, d], k and v: [T, Hkv, d], CUDA fp16/bf16, any strides the kernels can read (slices
     of one projection); query head h reads key head h // (Hq / Hkv).  ``softmax_scale <= 0``
-    selects 1/sqrt(d).  Sequences never touch each other, not even through NaN.  Within one, a
+    selects 1/sqrt(d).  Sequences never touch each other, not even through NaN.  A row that sees a
+    score of NaN or +inf is NaN in ``o`` and ``lse``; one of -inf weighs nothing.  A
     hidden key weighs exactly zero, so NaN or infinity in its v reaches the rows of its tile of 128
     tokens (cut from the sequence's end) as 0 * inf; rows of earlier tiles do not see it.
     Rows behind the last sequence of ``o`` and ``lse`` are left as they are

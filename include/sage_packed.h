@@ -113,8 +113,10 @@ typedef struct {
 /* Forward: o = softmax(softmax_scale q k^T) v within each sequence; lse [Hq][T] float32, the
  * natural log-sum-exp of the scaled scores.  Products of 16-bit values summed in float32; P is
  * rounded to dtype for the product with v.  Rows behind the last sequence are neither read
- * nor written.  Sequences never affect each other, whatever their values (a non-finite value may
- * reach any row of its own sequence).  The workspace (16-byte aligned) is needed where
+ * nor written.  Sequences never affect each other, whatever their values.  A row that
+ * sees a score of NaN or +inf is NaN in o and lse; a score of -inf weighs nothing, and a row with
+ * no other has o = NaN, lse = -inf.  A value that is not finite may also reach rows of its own
+ * sequence that do not see it, as 0 * inf.  The workspace (16-byte aligned) is needed where
  * sage_packed_attn_fwd_workspace_bytes is not 0: few heads and long sequences, whose walks over
  * the keys are cut into parts and joined. */
 size_t sage_packed_attn_fwd_workspace_bytes(const sage_packed_params* p,

@@ -36,6 +36,31 @@ def _run(q, k, v, do, batch, causal):
     return o, lse, dq, dk, dv
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads", [(2, 1), (3, 3)], ids=str)
+@pytest.mark.parametrize("d,dt", KINDS)
+def test_one_key_of_every_column(d, dt, heads, causal, value):
+    """128 sequences of three whole tiles; in sequence s, one channel of key 128 + s is planted."""
+    n, S = 384, 128
+    q, k, v, do = _inputs(n * S, *heads, d, dt, 80)
+    batch = packed.Batch([n] * S)
+    clean = _run(q, k, v, do, batch, causal)
+    bad = k.clone()
+    key = torch.arange(S, device="cuda") + 128
+    bad.view(S, n, heads[1], d)[torch.arange(S, device="cuda"), key, :, 0] = value
+    o, lse, dq, dk, dv = _run(q, bad, v, do, batch, causal)
+    row = torch.arange(n, device="cuda")
+    sees = (row >= key[:, None]).flatten() if causal else torch.ones(n * S, dtype=torch.bool,
+                                                                     device="cuda")
+    assert torch.isnan(o[sees]).all() and not torch.isfinite(lse[:, sees]).any()
+    assert torch.equal(o[~sees], clean[0][~sees])
+    assert torch.equal(lse[:, ~sees], clean[1][:, ~sees])
+    assert torch.isnan(dq[sees]).all()
+    # every key is seen by a row that sees the planted one
+    assert not torch.isfinite(dv).any() and not torch.isfinite(dk).any()
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("d,dt", KINDS)
 def test_one_query_of_every_column(d, dt, causal):
@@ -58,6 +83,27 @@ def test_one_query_of_every_column(d, dt, causal):
     assert not torch.isfinite(dv[seen]).any() and not torch.isfinite(dk[seen]).any()
     # a hidden key's P is exactly zero, and the row's dO is finite
     assert torch.equal(dv[~seen], clean[4][~seen])
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,dt", KINDS)
+def test_one_key_where_walks_are_cut_into_parts(d, dt, causal, value):
+    n = 4096
+    q, k, v, do = _inputs(n, 1, 1, d, dt, 82)
+    batch = packed.Batch([n])
+    assert packed.fwd_workspace_bytes(q, k, v, batch, causal) > 0
+    clean = _run(q, k, v, do, batch, causal)
+    for col in range(64):
+        key = 1280 + col + 64 * (col % 40)  # every column of a run of 64, over several parts
+        bad = k.clone()
+        bad[key, 0, 0] = value
+        o, lse, dq, dk, dv = _run(q, bad, v, do, batch, causal)
+        first = key if causal else 0
+        assert torch.isnan(o[first:]).all() and not torch.isfinite(lse[:, first:]).any(), key
+        assert torch.equal(o[:first], clean[0][:first]), key
+        assert torch.isnan(dq[first:]).all(), key
+        assert not torch.isfinite(dv).any() and not torch.isfinite(dk).any(), key
 
 
 @pytest.mark.parametrize("causal", [True, False])
