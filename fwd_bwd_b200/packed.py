@@ -14,7 +14,7 @@ import torch
 
 from ._lib import SageError, SagePackedInfo, SagePackedParams, check, lib
 from ._lib import SAGE_ERR_INVALID_ARG
-from .rope import _call, _like, _rows, _supported, _type_and_device
+from .rope import _call, _like, _readable, _rows, _type_and_device
 
 
 class Batch:
@@ -111,8 +111,8 @@ def attn_fwd(q, k, v, batch: Batch, causal: bool = True, softmax_scale: float = 
              ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention within each sequence (sage_packed_attn_fwd): (o [T, Hq, d], lse [Hq, T]).
 
-    q: [T, Hq, d], k and v: [T, Hkv, d], CUDA fp16/bf16, any strides the kernels can read (slices
-    of one projection); query head h reads key head h // (Hq / Hkv).  ``softmax_scale <= 0``
+    q: [T, Hq, d], k and v: [T, Hkv, d], CUDA fp16/bf16, 16-byte aligned, with any strides the
+    kernels can read (slices of one projection); query head h reads key head h // (Hq / Hkv).  ``softmax_scale <= 0``
     selects 1/sqrt(d).  Sequences never touch each other, not even through NaN.  A row that sees a
     score of NaN or +inf is NaN in ``o`` and ``lse``; one of -inf weighs nothing.  A
     hidden key weighs exactly zero, so NaN or infinity in its v reaches the rows of its tile of 128
@@ -200,7 +200,7 @@ def fwd_workspace_bytes(q, k, v, batch: Batch, causal: bool = True) -> int:
 class _PackedAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, batch, causal, softmax_scale):
-        q, k, v = (x if _supported(x) else x.contiguous() for x in (q, k, v))
+        q, k, v = (_readable(x) for x in (q, k, v))
         o, lse = attn_fwd(q, k, v, batch, causal, softmax_scale)
         ctx.save_for_backward(q, k, v, o, lse)
         ctx.args = (batch, causal, softmax_scale)
@@ -210,13 +210,13 @@ class _PackedAttention(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, o, lse = ctx.saved_tensors
-        dout = dout if _supported(dout) else dout.contiguous()
-        dq, dk, dv = attn_bwd(q, k, v, o, lse, dout, *ctx.args)
+        dq, dk, dv = attn_bwd(q, k, v, o, lse, _readable(dout), *ctx.args)
         return dq, dk, dv, None, None, None
 
 
 def packed_attention(q, k, v, batch: Batch, causal: bool = True, softmax_scale: float = 0.0):
-    """``attn_fwd`` with autograd: o [T, Hq, d]."""
+    """``attn_fwd`` with autograd: o [T, Hq, d].  Tensors and gradients that the kernels cannot read
+    where they are (off a 16-byte boundary, or with other strides) are copied."""
     return _PackedAttention.apply(q, k, v, batch, causal, softmax_scale)
 
 

@@ -72,6 +72,14 @@ def _supported(x: torch.Tensor) -> bool:
                for n, s in zip(x.shape[:-1], x.stride()[:-1]))
 
 
+def _readable(x: torch.Tensor) -> torch.Tensor:
+    """x, or a copy of it where the kernels cannot read it as it is."""
+    if _supported(x):
+        return x
+    y = x.contiguous()  # x itself when only its address is off
+    return y if _supported(y) else y.clone()
+
+
 def _rows(x: torch.Tensor) -> SageRows:
     """The tensor's description for the C ABI, which checks pointers, alignment, the other strides
     and overlap within an output."""
@@ -222,8 +230,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, rope: Rope, gain_q=None, g
 class _QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, positions, rope, gain_q, gain_k):
-        q = q if _supported(q) else q.contiguous()
-        k = k if _supported(k) else k.contiguous()
+        q, k = _readable(q), _readable(k)
         gains = [None if g is None else g.detach().float().contiguous() for g in (gain_q, gain_k)]
         gains = [g if g is None or g.data_ptr() % 16 == 0 else g.clone() for g in gains]
         ctx.save_for_backward(q, k, positions, *gains)
@@ -235,15 +242,16 @@ class _QkNormRope(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, positions, gq, gk = ctx.saved_tensors
-        dq_out = dq_out if _supported(dq_out) else dq_out.contiguous()
-        dk_out = dk_out if _supported(dk_out) else dk_out.contiguous()
-        dq, dk, dgq, dgk = qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, ctx.rope, gq, gk)
+        dq, dk, dgq, dgk = qk_norm_rope_bwd(q, k, _readable(dq_out), _readable(dk_out), positions,
+                                            ctx.rope, gq, gk)
         dgains = [None if t is None else g.to(t) for g, t in zip((dgq, dgk), ctx.gain_dtypes)]
         return dq, dk, None, None, dgains[0], dgains[1]
 
 
 def qk_norm_rope(q, k, positions, rope: Rope, gain_q=None, gain_k=None):
-    """``qk_norm_rope_fwd`` with autograd, for q, k and the gains (of any floating type)."""
+    """``qk_norm_rope_fwd`` with autograd, for q, k and the gains (of any floating type).  Tensors and
+    gradients that the kernels cannot read where they are (off a 16-byte boundary, or with other
+    strides) are copied."""
     return _QkNormRope.apply(q, k, positions, rope, gain_q, gain_k)
 
 

@@ -1,0 +1,18 @@
+"""Host side of the packed operators' arguments (no GPU)."""
+import torch
+
+from fwd_bwd_b200 import rope
+
+
+def test_copies_only_what_the_kernels_cannot_read():
+    store = torch.randn(4 * 3 * 64 + 8).bfloat16()
+    x = store[:4 * 3 * 64].view(4, 3, 64)
+    assert x.data_ptr() % 16 == 0
+    for same in (x, x[:, 1:], x[::2], x.transpose(0, 1), x[:1], x[:0]):
+        assert rope._readable(same) is same
+    off = store[1:1 + 4 * 3 * 64].view(4, 3, 64)
+    for y in (off, off[:, 1:], off[:, 1:2], off.transpose(0, 1), x[..., :1].expand(-1, -1, 64),
+              x[:, :1].expand(-1, 3, -1), x.transpose(1, 2).contiguous().transpose(1, 2)):
+        z = rope._readable(y)
+        assert torch.equal(z, y) and rope._supported(z)
+        assert z.data_ptr() % 16 == 0 and z.data_ptr() != y.data_ptr()
