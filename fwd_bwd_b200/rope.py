@@ -125,6 +125,8 @@ def _params(q, k, positions, rope: Rope, gains) -> Tuple[SageRopeParams, Optiona
         raise ValueError("q and k must have one layout, type and device")
     if (ks[0] != qs[0] or ks[-1] != d or d != rope.d or (len(qs) == 4 and ks[2] != N)):
         raise ValueError("q and k must hold the same tokens, with rope.d channels")
+    if (Hq == 0) != (Hkv == 0) and B * N:
+        raise ValueError("q and k must both have heads")
     for g in gains:
         if g is None:
             continue

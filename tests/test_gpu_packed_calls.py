@@ -63,3 +63,19 @@ def test_rotary_autograd_of_tensors_off_their_alignment(by):
         got = run(*(_off(t, by) if i in which else t for i, t in enumerate(x)))
         for a, b in zip(got, want):
             assert torch.equal(a, b), which
+
+
+def test_one_tensor_without_heads_is_refused():
+    """Not taken for nothing to do, which would leave the other's outputs unwritten."""
+    T, rp = 10, rope.Rope(64)
+    some, none = _random(T, 2, 64, 0), _random(T, 0, 64, 0)
+    pos = torch.arange(T, device="cuda")
+    for q, k in ((none, some), (some, none)):
+        with pytest.raises(ValueError, match="heads"):
+            rope.qk_norm_rope_fwd(q, k, pos, rp)
+        with pytest.raises(ValueError, match="heads"):
+            rope.qk_norm_rope_bwd(q, k, q, k, pos, rp)
+        with pytest.raises(ValueError, match="heads"):
+            rope.qk_norm_rope(q[None].transpose(1, 2), k[None].transpose(1, 2), pos, rp)
+    for x in rope.qk_norm_rope_fwd(none, none, pos, rp):
+        assert x.shape == (T, 0, 64)
