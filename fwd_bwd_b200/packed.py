@@ -8,6 +8,7 @@ their lengths and the plan the kernels work from.  ``packed_attention`` is the a
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -33,7 +34,10 @@ class Batch:
             if lengths.is_floating_point() or lengths.dim() != 1:
                 raise ValueError("lengths must be a 1-D sequence of integers")
             lengths = lengths.tolist()
-        self.lengths = [int(n) for n in lengths]
+        try:
+            self.lengths = [operator.index(n) for n in lengths]
+        except TypeError:
+            raise ValueError("lengths must be a 1-D sequence of integers") from None
         if not self.lengths or min(self.lengths) < 0 or max(self.lengths) >= 2 ** 31:
             raise ValueError("lengths must be a non-empty sequence of integers >= 0")
         arr = (ctypes.c_int * len(self.lengths))(*self.lengths)

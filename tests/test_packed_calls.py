@@ -1,7 +1,9 @@
 """Host side of the packed operators' arguments (no GPU)."""
+import numpy as np
+import pytest
 import torch
 
-from fwd_bwd_b200 import rope
+from fwd_bwd_b200 import packed, rope
 
 
 def test_copies_only_what_the_kernels_cannot_read():
@@ -16,3 +18,15 @@ def test_copies_only_what_the_kernels_cannot_read():
         z = rope._readable(y)
         assert torch.equal(z, y) and rope._supported(z)
         assert z.data_ptr() % 16 == 0 and z.data_ptr() != y.data_ptr()
+
+
+@pytest.mark.parametrize("lengths", [[2.5], [3.0, 1], np.array([2.0, 7.9]), ["4"], [None]], ids=str)
+def test_lengths_that_are_not_integers_are_refused(lengths):
+    with pytest.raises(ValueError, match="integers"):
+        packed.Batch(lengths, device="cpu")
+
+
+def test_lengths_of_every_integer_type():
+    for lengths in (np.array([3, 0, 5]), np.array([3, 0, 5], np.uint8), (3, 0, 5),
+                    torch.tensor([3, 0, 5]), list(torch.tensor([3, 0, 5], dtype=torch.int32))):
+        assert packed.Batch(lengths, device="cpu").lengths == [3, 0, 5]
