@@ -20,9 +20,10 @@
 // instructions (180 per two rows of 128 channels, 61% of the issue slots, 16 warps to an SM).
 //
 // Angles: frequency i as F_i = inv_freq_i / (2 pi) * 2^64 modulo 2^64, so position * F_i
-// modulo 2^64 is the angle's fraction of a turn, with all full turns dropped exactly: the same
-// accuracy at position 2^31 as at 1.  Its top 32 bits, a signed fraction of a half turn, become
-// an angle in [-pi, pi], where the fast sine and cosine are within 2^-21 of the true ones (they
+// modulo 2^64 is the angle's fraction of a turn, with all full turns dropped exactly.  F_i is rounded
+// to a whole number, which moves the angle by 2 pi |position| 2^-65: 2^-31 at position 2^31, 2^-22 at
+// 2^40.  The top 32 bits, a signed fraction of a half turn, become a float angle in [-pi, pi]
+// (three roundings of 2^-24 pi), whose fast sine and cosine are within 2^-21: 2^-20 in all (they
 // multiply values that are rounded to 2^-9 or 2^-11 afterwards).
 #pragma once
 

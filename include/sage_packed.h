@@ -46,8 +46,10 @@ typedef struct {
  * gains are left out.  R turns pairs of the first rotary_dim channels; pair i is channels
  * (i, i + rotary_dim/2), or (2i, 2i + 1) when interleaved; its angle is pos_a * inv_freq[i]
  * radians, where a is the position axis whose section holds i: the n_axes sections (pairs per
- * axis, none empty, in order) add up to rotary_dim/2.  The angle's full turns are dropped
- * exactly (64-bit fixed-point turns), so positions may be as far as 64 bits reach. */
+ * axis, none empty, in order) add up to rotary_dim/2.  Turns are 64-bit fixed-point fractions,
+ * so full ones drop out exactly, but inv_freq / (2 pi) is rounded to 2^-64 turns (relatively, where
+ * it is above 1): the angle is off by up to 2 pi |pos| 2^-64, which passes the kernel's own 2^-20
+ * from |pos| = 2^41 on. */
 typedef struct {
   int B, N, Hq, Hkv, d;
   int dtype;               /* sage_dtype of x, y and their gradients                      */
@@ -75,7 +77,7 @@ int sage_qk_norm_rope_fwd(const sage_rope_params* p, const sage_rows* q, const s
  *   g = R^T dy;  dgain_c = sum over tokens and heads of g_c xhat_c;  gx = g gain;
  *   dx = inv (gx - xhat mean_c(gx xhat)).
  * dgain_q, dgain_k (float32 [d], both or none; only with norm): sums in a fixed order, so the
- * result is the same from call to call.  The workspace (256-byte aligned,
+ * result is the same from call to call.  The workspace (16-byte aligned,
  * sage_qk_norm_rope_workspace_bytes) is needed only with dgain. */
 size_t sage_qk_norm_rope_workspace_bytes(const sage_rope_params* p);
 int sage_qk_norm_rope_bwd(const sage_rope_params* p, const sage_rows* q, const sage_rows* k,
