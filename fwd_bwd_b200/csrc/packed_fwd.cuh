@@ -35,7 +35,8 @@
 // by the row sum, and most key tiles leave O untouched.
 // A row that sees a score of NaN or +inf is NaN in O and LSE: the maximum keeps NaN, and the row's
 // exponentials, sum and rescaled O are NaN from that tile on.
-// Rounding: P to the tensors' type for P V (the sum l uses the unrounded P); O once at the end.
+// Rounding: P (in half precision times 2^7, kFwdShift) to the tensors' type for P V (the sum l uses
+// the unrounded P); O once at the end.
 // A quarter of the exponentials runs on the FMA pipe (32 heads of 128, prompts of 4099 to 8 tokens:
 // 222 us, 224 us with an eighth, 225 us with none; d = 64, images: 38 us against 39 us).
 //
@@ -205,10 +206,17 @@ __device__ __forceinline__ float2 exp2_fma2(float2 z) {
                      __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
 }
 
+// log2 of the factor that the forward's P (and with it l and O) carries: half precision's normal
+// numbers end at 2^-14, so P, at most 2^8, is taken times 2^7: weights down to 2^-21 of the row's
+// largest keep all bits.
+template <typename T>
+constexpr float kFwdShift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
+
 // What the scores of a row are shifted by: -m; 0 while no key weighs anything (m = -inf), so that
-// -inf stays -inf; NaN for a maximum of +inf, whose row has no softmax.
+// -inf stays -inf; NaN for a maximum of +inf, whose row has no softmax.  P's factor comes on top.
+template <typename T>
 __device__ __forceinline__ float neg_max(float m) {
-  return m == -INFINITY ? 0.0f : fmaf(m, 0.0f, -m);
+  return kFwdShift<T> + (m == -INFINITY ? 0.0f : fmaf(m, 0.0f, -m));
 }
 
 // Pairs whose exponentials run on the FMA pipe.
@@ -532,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const float neg = neg_max(m);
+      const float neg = neg_max<T>(m);
       const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
       float2 sum = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -577,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (i >= 0 && (g == 0 || two)) {
       const int64_t row = static_cast<int64_t>(it.start) + i;
-      res = row_out<T, D, PARTS>(a, row, HEADS ? head0 + g : head0, split, m, l);
+      res = row_out<T, D, PARTS>(a, row, HEADS ? head0 + g : head0, split, m - kFwdShift<T>, l);
     }
     if (n > 0) {
 #pragma unroll
@@ -767,7 +775,7 @@ __global__ void __launch_bounds__(kThreads64, 4)
           }
         }
       }
-      const float neg = neg_max(m);
+      const float neg = neg_max<T>(m);
       const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
       float2 sum = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -801,7 +809,7 @@ __global__ void __launch_bounds__(kThreads64, 4)
     if (!PARTS || n > 0) mbar_wait(&sm.o_full, 0, 352);
     tc_fence_after();
     RowOut<T, PARTS> res = {};
-    if (i >= 0) res = row_out<T, D, PARTS>(a, static_cast<int64_t>(it.start) + i, head, split, m, l);
+    if (i >= 0) res = row_out<T, D, PARTS>(a, static_cast<int64_t>(it.start) + i, head, split, m - kFwdShift<T>, l);
     if (!PARTS || n > 0) {
 #pragma unroll
       for (int cc = 0; cc < D; cc += 32) {
