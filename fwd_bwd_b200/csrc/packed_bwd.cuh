@@ -36,9 +36,9 @@
 //
 // Rounding: P and dS to the tensors' type for their products; sums in float32; outputs once.
 // Half precision: P is multiplied by 2^14 before it is rounded, and dS by the power of two that
-// puts the bound 2 max |dO_i| max |v_j| of |dP - D| (over the sequence and key head) at 2^15 or
-// just below: small values keep their bits, nothing overflows, and the factors are taken out of
-// the float32 sums exactly.
+// puts the bound 2 max |dO_i| max |v_j| of |dP - D| (over the finite rows of the sequence and key
+// head) at 2^15 or just below: small values keep their bits, nothing overflows, and the factors
+// are taken out of the float32 sums exactly.
 #pragma once
 
 #include "packed_fwd.cuh"
@@ -80,7 +80,7 @@ struct RowArgs {
   Out o, dout, v;        // inputs
   const Item* items;
   float* dvec;           // [Hq][T]
-  uint32_t* norms;       // [sequences][Hkv][2]: bits of max |dO|^2, max |v|^2 (zeroed before)
+  uint32_t* norms;       // [sequences][Hkv][2]: bits of max |dO|^2, max |v|^2, finite (zeroed before)
   int64_t T;
   int tiles, Hq, Hkv, group;
 };
@@ -129,15 +129,16 @@ __global__ void __launch_bounds__(kRowKernelThreads) row_kernel(const RowArgs a)
     dot[s] = row_sum<LPR>(p, mask);
     if (NORMS) {
       q = row_sum<LPR>(q, mask);
-      most = q > most || q != q ? q : most;  // a NaN stays
+      // what is not finite says nothing: the rows that see it have no finite gradient anyhow
+      if (q > most && q < INFINITY) most = q;
     }
     const int i = row_index(it, it.tile, r0 + s * ROWS);
     if (!on_v && l == 0 && i >= 0) a.dvec[head * a.T + it.start + i] = dot[s];
   }
   if (NORMS) {
-    // float bits of non-negative values (and NaN above all) order like unsigned integers, and a
-    // maximum does not depend on the order
-    uint32_t m = __float_as_uint(most) & 0x7fffffffu;
+    // float bits of non-negative values order like unsigned integers, and a maximum does not depend
+    // on the order
+    uint32_t m = __float_as_uint(most);
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) {
       const int kv = on_v ? head : head / a.group;
@@ -146,10 +147,10 @@ __global__ void __launch_bounds__(kRowKernelThreads) row_kernel(const RowArgs a)
   }
 }
 
-// The factor of dS (a power of two) from the two norms; 1 where they say nothing.
+// The factor of dS (a power of two) from the two norms; 1 where one is zero.
 __device__ __forceinline__ float ds_factor(const uint32_t* norms) {
   const float b = 2.0f * sqrtf(__uint_as_float(norms[0])) * sqrtf(__uint_as_float(norms[1]));
-  if (!(b > 0.0f) || b > 3.0e38f) return 1.0f;
+  if (!(b > 0.0f)) return 1.0f;  // at most 2^40 otherwise
   int e = 14 - ilogbf(b);  // b 2^e in [2^14, 2^15)
   e = max(-60, min(60, e));
   return scalbnf(1.0f, e);
