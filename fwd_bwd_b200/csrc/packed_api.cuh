@@ -296,8 +296,12 @@ int launch_packed(int64_t grid, int threads, size_t smem, cudaStream_t st, const
 // item takes, because the last chunk's long items start late (16384 tokens in documents of
 // 5021 to 2, 4 key heads, dK/dV: 330 us in one chunk, 442 us in four).
 constexpr int64_t kChunkBytes = 40 << 20;  // of the 126 MB L2
-// What is this small in all stays there anyway (8 x 2048 tokens, 16 heads of 64, 67 MB: forward 118
-// -> 114 us, dQ 140 -> 137, dK/dV 182 -> 178 us in one chunk instead of two).
+// What is this small in all is taken in one chunk: a second one ends the first with a tail and no
+// longer pays by its hits. One chunk against chunks of 40 MB (forward, dQ, dK/dV, us):
+//   d = 64, 2048 tokens x 8:   50 MB  89, 106, 144 / 105, 114, 151;  67 MB 112, 135, 176 / 114, 138, 180;
+//                             84 MB 140, 168, 220 / 138, 169, 224; 101 MB 170, 203, 272 / 176, 204, 280
+//   d = 128, 4096 tokens x 2:  50 MB 104, 143, 168 / 130, 163, 178;  75 MB 143, 218, 251 / 145, 214, 249;
+//                             84 MB 160, 243, 282 / 158, 235, 272; 101 MB 192, 300, 349 / 201, 281, 331
 constexpr int64_t kAllBytes = 80 << 20;
 int grid_chunk(const sage_packed_params* p, const sage_packed_info* info, int heads,
                int64_t bytes_per_head) {
@@ -313,10 +317,12 @@ int grid_chunk(const sage_packed_params* p, const sage_packed_info* info, int he
 // Parts that a kernel's walks are cut into.  A CTA walks all the tiles its own tile meets; with few
 // heads that leaves SMs idle or one long walk at the end.  Cut when the longest walk (steps) is
 // twice the device's share of all of them or more, into parts of eight steps at least, eight parts
-// at most (each costs 8 bytes of traffic per element of the output, and the joining kernel some 4 us;
-// 2048 tokens, 32 query heads on one key head of 128: dK/dV 621 -> 95 + 4 us; 8192 tokens, one
-// head: 89 -> 51 + 7 us, forward 99 -> 34 us; where the longest walk is 1.1 times the share, 32 heads
-// on one, cutting costs: forward 43 -> 69 us).
+// at most (each costs 8 bytes of traffic per element of the output, and the joining kernel 4 to 10
+// us).  Whole / cut, us with the joining kernel:
+//   8192 tokens, 1 head of 128:   forward 99 / 36 + 7, dQ 76 / 32 + 5, dK/dV 88 / 41 + 7
+//   2048 tokens, 32 heads on one key head of 128: dK/dV 621 / 94 + 4
+//   4096 tokens, heads of 128, forward: 4 heads (longest 4.5 x the share) 57 / 38 + 7; 8 heads (2.2 x)
+//     58 / 50 + 10; cut from the share on: 12 heads (1.5 x) 61 / 92 + 20, 16 heads (1.1 x) 67 / 95 + 20
 int walk_splits(int64_t longest, int64_t all, int places) {
   const int64_t share = std::max<int64_t>(1, all / places);
   return static_cast<int>(std::max<int64_t>(

@@ -9,9 +9,11 @@
 //   * dkv_kernel: one CTA per (key tile, key head), walking the query tiles of every head of the
 //     group.  It works on transposed tiles (rows = keys), so P^T and dS^T go from registers to
 //     TMEM as the A operands of dV += P^T dO and dK += dS^T Q, and dV, dK stay in TMEM.
-// Seven products where one fused pass would need five, but no gradient is ever added up across
-// CTAs: no atomics, no float32 accumulator in HBM, no finishing pass, the same bits every run,
-// and grouped heads cost nothing extra.
+// Seven products where one fused pass would need five, but a gradient is summed by one CTA: no
+// atomics, no float32 accumulator in HBM, no finishing pass, the same bits every run, and grouped
+// heads cost nothing extra.  Only where walks are cut into parts (few heads, long walks) do several
+// CTAs share a sum: each part's float32 sums go to the workspace, for every token of the batch, and
+// join_kernel adds them in the parts' order: the same bits every run there too.
 //
 // Both work on blocks of 128 rows x D columns (the walked side in runs of D rows).  d = 128 fills
 // TMEM and shared memory: one CTA per SM.  d = 64 takes half of both, so two CTAs share an SM and
