@@ -59,6 +59,10 @@ class Batch:
             self._stream = stream.cuda_stream
         self.tokens = int(self.info.tokens)
 
+    def __reduce__(self):
+        """Copies are made anew: a plan of their own, complete before they are used."""
+        return type(self), (self.lengths, self.device)
+
     def _used_on(self, stream: torch.cuda.Stream) -> None:
         """Keeps the plan's memory from its allocating stream while another one reads it."""
         if stream.cuda_stream != self._stream:

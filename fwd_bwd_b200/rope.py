@@ -58,6 +58,11 @@ class Rope:
         self._freq_ptr = ctypes.addressof(self._freq)
         self._sections = (ctypes.c_int * 4)(*(self.sections if half else []))
 
+    def __reduce__(self):
+        """Copies are made anew: the library reads frequencies at an address of their own."""
+        return type(self), (self.d, 1.0, self.rotary_dim, self.sections if self.rotary_dim else None,
+                            self.interleaved, self.inv_freq, self.norm, self.eps)
+
     @property
     def axes(self) -> int:
         return len(self.sections) if self.rotary_dim else 0

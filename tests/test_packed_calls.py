@@ -1,4 +1,8 @@
 """Host side of the packed operators' arguments (no GPU)."""
+import copy
+import ctypes
+import pickle
+
 import numpy as np
 import pytest
 import torch
@@ -30,3 +34,25 @@ def test_lengths_of_every_integer_type():
     for lengths in (np.array([3, 0, 5]), np.array([3, 0, 5], np.uint8), (3, 0, 5),
                     torch.tensor([3, 0, 5]), list(torch.tensor([3, 0, 5], dtype=torch.int32))):
         assert packed.Batch(lengths, device="cpu").lengths == [3, 0, 5]
+
+
+def _copies(x):
+    return copy.copy(x), copy.deepcopy(x), pickle.loads(pickle.dumps(x))
+
+
+def test_copies_of_a_batch_use_their_own_plan():
+    b = packed.Batch([300, 0, 5], device="cpu")
+    for c in _copies(b):
+        assert c.plan_ptr == c.plan.data_ptr()
+        assert c.lengths == b.lengths and c.tokens == b.tokens and torch.equal(c.plan, b.plan)
+        assert bytes(c.info) == bytes(b.info) and c.device == b.device
+        assert c.positions().tolist() == b.positions().tolist()
+
+
+def test_copies_of_a_rope_use_their_own_frequencies():
+    r = rope.Rope(64, rotary_dim=32, sections=[5, 11], interleaved=True, eps=1e-5)
+    for c in _copies(r):
+        assert c._freq_ptr == ctypes.addressof(c._freq)
+        assert list(c._freq) == r.inv_freq == c.inv_freq and list(c._sections) == [5, 11, 0, 0]
+        assert (c.d, c.rotary_dim, c.axes, c.interleaved, c.norm, c.eps) == (64, 32, 2, True, True,
+                                                                             1e-5)
