@@ -33,7 +33,7 @@
 // visible scores):
 //   d = 128, 4 x 8192, 16 heads, bf16    dQ 1277 us, 1291 TFLOP/s   dK/dV 1527 us, 1440 TFLOP/s
 //   d = 64, 8 x 2048, 16 heads           dQ  134 us,  772 TFLOP/s   dK/dV  171 us,  804 TFLOP/s
-// Bound: d = 128 by the chain of products and exponentials of one tile (tensor pipe 54% and 66%
+// Bound: d = 128 by the chain of products and exponentials of one tile (tensor pipe 52% and 64%
 // active) and, in longer runs, by the power cap; d = 64 by the chains of two CTAs (36%, 38%).
 //
 // Rounding: P and dS to the tensors' type for their products; sums in float32; outputs once.

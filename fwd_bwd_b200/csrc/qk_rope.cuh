@@ -17,7 +17,7 @@
 // Measured (B200): 262144 tokens, 20 heads of 128: forward 459 us (5.8 TB/s), backward 836 us (4.8
 // TB/s, against 875 us with rows loaded to registers where they are used); 16384 tokens, 32 heads
 // of 64: 30 us and 46 us; a copy runs at 6.5 TB/s.  What keeps the backward from that is latency:
-// 125 registers leave 16 warps to an SM, and neither the issue slots (61%) nor DRAM (58%) are full.
+// 125 registers leave 16 warps to an SM, and neither the issue slots (60%) nor DRAM (60%) are full.
 //
 // Angles: frequency i as F_i = inv_freq_i / (2 pi) * 2^64 modulo 2^64, so position * F_i
 // modulo 2^64 is the angle's fraction of a turn, with all full turns dropped exactly.  F_i is rounded
